@@ -128,9 +128,9 @@ def _prepare_distill(case, gen):
     if k > 8:  # some rows have kept fewer
         ids[::5, k - 3:] = -1
     w = None
-    if case["weighted"]:  # the mean over the tokens that count
-        w = (torch.rand(T, generator=gen, device="cuda") < 0.9).float()
-        w[0] = 1.0
+    if case["weighted"]:  # the mean over the tokens that count; every tenth is padding
+        w = torch.ones(T, device="cuda")
+        w[9::10] = 0.0
         w /= w.sum()
     return dict(case=case, Z=z[:, :V], ids=ids, vals=vals, w=w, tau=case["tau"])
 
@@ -204,6 +204,8 @@ def _plain_distill(s):
     total = e.sum(1, keepdim=True)
     log_p = x.gather(1, ids) - torch.log(total)
     out = {"loss": s["tau"] ** 2 * torch.where(q > 0, q * (log_q - log_p), 0.0).sum(1)}
+    if s["w"] is not None:  # padding is left out
+        out["loss"] = torch.where(s["w"] != 0, out["loss"], 0.0)
     if s["case"]["grad"]:
         g = e / total
         g.scatter_add_(1, ids, -q)
@@ -286,8 +288,11 @@ def work(case):
         T, n = case["T"], case["T"] * case["V"]
         if case["op"] == "logprobs":
             return {"bytes": n * b + T * (12 + 8 * case["top"]), "flops": 6 * n}
-        passes = 2 if case["grad"] else 1
-        return {"bytes": passes * n * b + T * (8 * case["k"] + 8), "flops": 4 * passes * n}
+        # padding rows are not read, their gradient is written as zeros
+        live = n - (T // 10 * case["V"] if case["weighted"] else 0)
+        back = n if case["grad"] else 0
+        return {"bytes": (live + back) * b + T * (8 * case["k"] + 8),
+                "flops": 4 * live * (2 if back else 1)}
     lens = [int(x) for x in case["lengths"].split(",")]
     T, H, G, d_h = sum(lens), case["heads"], case["kv_heads"], case["d_h"]
     pairs = sum(n * (n + 1) // 2 for n in lens)
@@ -327,6 +332,8 @@ def _exact_distill(s):
         if s["case"]["grad"]:
             w = torch.ones_like(loss) if s["w"] is None else s["w"][a:a + 256].double()
             grads.append(torch.autograd.grad((loss * w).sum(), z)[0])
+        if s["w"] is not None:
+            loss = loss * (s["w"][a:a + 256] != 0)
         losses.append(loss.detach())
     out = {"loss": torch.cat(losses)}
     if grads:
