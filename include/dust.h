@@ -287,6 +287,116 @@ dust_status dust_attn_grad(dust_ctx* ctx, const dust_params* p, const dust_attn_
                            const void* X, const float* Q, const float* Kc, const float* Vc,
                            const float* E, float* G_out, float* rewards_out, float* g_out);
 
+/*
+ * Scores of logits that a model has already produced: per row of Z the log
+ * probability of a given token, the entropy (natural log) and the `top` most
+ * likely tokens.
+ *   Z        T x V logits (dtype DUST_F32 or DUST_BF16), row t at Z + t ldz
+ *            elements, ldz >= V; any alignment of whole elements
+ *   tokens   T int32 in [0, V), or -1 where a row has no token (its logp is
+ *            0); NULL when logp_out is NULL
+ *   logp_out T, entropy_out T                              fp32 (or NULL)
+ *   top_ids_out T x top int32, top_logp_out T x top fp32   (both or neither;
+ *            neither when top = 0): by descending logit, equal ones by the
+ *            lower index; top <= 128
+ * Logits of -inf are masked tokens: log probability -inf, nothing in the
+ * entropy, never an alternative. Where a row has fewer than `top` other
+ * logits, the rest of its alternatives are id -1 with log probability -inf; a
+ * row of -inf alone has logp -inf and entropy 0. A row that holds NaN or +inf
+ * has no distribution: logp, entropy and top_logp are NaN, its ids -1.
+ * Needs no scratch. T = 0 launches nothing. flags: DUST_FLAG_ASYNC. The call
+ * does not clear the status that earlier DUST_FLAG_ASYNC calls left.
+ * Errors: DUST_ERR_ARG, DUST_ERR_BOUNDS (a token outside [-1, V): its logp is NaN).
+ */
+dust_status dust_token_logprobs(dust_ctx* ctx, int64_t T, int64_t V, int32_t dtype, const void* Z,
+                                int64_t ldz, const int32_t* tokens, int32_t top, float* logp_out,
+                                float* entropy_out, int32_t* top_ids_out, float* top_logp_out,
+                                uint32_t flags);
+
+/*
+ * Distillation from a teacher's top logits, forward and backward. With
+ * q = softmax(v / temperature) over the k entries that the teacher kept of a
+ * row and p = softmax(z / temperature) over the student's vocabulary,
+ *   loss_t = temperature^2 sum_j q_j (log q_j - log p_j),
+ *   dZ_t   = w_t temperature (p - q)            (q = 0 off the kept entries),
+ * the gradient of sum_t w_t loss_t.
+ *   Z        T x V student logits as for dust_token_logprobs
+ *   teacher_ids  T x k int32 in [0, V), or -1: no entry; 1 <= k <= 128. An id
+ *            listed twice carries both weights.
+ *   teacher_vals T x k fp32 logits or log probabilities (a constant per row
+ *            cancels); -inf: no entry. dust_token_logprobs' alternatives of the
+ *            teacher's logits can be passed as they are.
+ *   weights  T fp32, or NULL: all 1
+ *   loss_out T fp32 (or NULL): not multiplied by the weights
+ *   dZ_out   T x V in Z's dtype (or NULL), row t at dZ_out + t lddz, lddz >= V;
+ *            dZ_out = Z with lddz = ldz writes the gradient over the logits,
+ *            any other overlap is not allowed
+ * A row without a teacher entry, or of weight 0, is left out: loss 0, gradient
+ * 0, and its logits are not read. A masked student logit (-inf) has p = 0; the
+ * loss is +inf where the teacher keeps it. NaN and +inf logits of a row make
+ * its loss and gradient NaN. The gradient is formed in fp32 and rounded once.
+ * Needs no scratch. T = 0 launches nothing. flags as dust_token_logprobs.
+ * Errors: DUST_ERR_ARG, DUST_ERR_BOUNDS (a teacher id outside [-1, V), which
+ * counts as no entry), DUST_ERR_TIMEOUT.
+ */
+dust_status dust_distill(dust_ctx* ctx, int64_t T, int64_t V, int32_t dtype, const void* Z,
+                         int64_t ldz, const int32_t* teacher_ids, const float* teacher_vals,
+                         int32_t k, float temperature, const float* weights, float* loss_out,
+                         void* dZ_out, int64_t lddz, uint32_t flags);
+
+/*
+ * Causal multi-head attention over packed sequences, and its exact gradient:
+ * what dust_attn_grad's estimate converges to for an error signal E.
+ *   o_i = sum_{j <= i} softmax_j(scale <q_i, k_j>) v_j inside each sequence.
+ * All tensors are rows of tokens with the heads side by side (head h in
+ * columns [h head_dim, (h+1) head_dim)), with a row stride each, so the parts
+ * of one fused projection can be passed as they are. Query heads h of
+ * n_heads / n_kv_heads consecutive ones share a key/value head.
+ */
+typedef struct dust_attn_dims {
+  int64_t T;                 /* rows of the tensors */
+  const int32_t* cu_seqlens; /* DEVICE, n_seqs + 1 non-decreasing row offsets in
+                                [0, T]; NULL: n_seqs sequences of max_len rows */
+  int32_t n_seqs;            /* sequences (0: nothing is launched), at most 65535 */
+  int32_t max_len;           /* longest sequence (>= 1) */
+  int32_t n_heads, n_kv_heads; /* n_heads a multiple of n_kv_heads, at most 65535 */
+  int32_t head_dim;          /* 32, 64 or 128 */
+  int32_t dtype;             /* of every tensor but lse: DUST_F32 or DUST_BF16 */
+  float scale;               /* finite and > 0; 0: 1 / sqrt(head_dim) */
+  uint32_t flags;            /* DUST_FLAG_ASYNC */
+  int64_t ldq, ldk, ldv, ldo, lde, lddq, lddk, lddv; /* row strides, elements */
+} dust_attn_dims;
+/* Forward.
+ *   Q T x (n_heads head_dim), Kc and Vc T x (n_kv_heads head_dim)
+ *   O_out   like Q; lse_out T x n_heads fp32, log-sum-exp of a row's scores
+ * Rows that no sequence covers (behind the last one, say) are neither read nor
+ * written, and neither is anything of one sequence mixed into another, NaN
+ * included. Values that are not finite spread inside their own sequence.
+ * fp32 tensors are computed in fp32. bf16 tensors: products with fp32
+ * accumulation, softmax in fp32, the probabilities rounded to bf16 for the
+ * product with V; outputs are rounded once.
+ * Needs no scratch. lse_out must not be NULL. flags as dust_token_logprobs.
+ * Errors: DUST_ERR_ARG, DUST_ERR_BOUNDS (offsets that decrease, leave [0, T]
+ * or make a sequence longer than max_len: that sequence is skipped),
+ * DUST_ERR_TIMEOUT. */
+dust_status dust_attn_forward(dust_ctx* ctx, const dust_attn_dims* dims, const void* Q,
+                              const void* Kc, const void* Vc, void* O_out, float* lse_out);
+/* Backward: gradients of sum_t <o_t, e_t>.
+ *   Q, Kc, Vc, O, lse  as given to and returned by dust_attn_forward
+ *   E        like Q: the error signal (gradient) at the attention output
+ *   dQ_out   like Q; dK_out, dV_out like Kc (sums over the heads that share
+ *            a key/value head); dtype as the inputs, rounded once
+ *   delta    T x n_heads fp32 scratch of the caller, overwritten. The call
+ *            has no scratch of its own, so calls and captured graphs that
+ *            overlap need only a delta each.
+ * The probabilities are recomputed from lse; no sum uses atomics, so results
+ * are the same from run to run. Outputs must not overlap the inputs.
+ * Errors as dust_attn_forward. */
+dust_status dust_attn_backward(dust_ctx* ctx, const dust_attn_dims* dims, const void* Q,
+                               const void* Kc, const void* Vc, const void* O, const float* lse,
+                               const void* E, void* dQ_out, void* dK_out, void* dV_out,
+                               float* delta);
+
 /* Per-stage device timing: when enabled, each call records CUDA events on
    the context's stream between its stages (clean GEMM, log-sum-exp, draws,
    g, G_W GEMM...). dust_stage_times waits for the last call's final event

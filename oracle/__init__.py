@@ -57,3 +57,4 @@ from .mlp import (  # noqa: F401
 )
 from .optim import sgd_momentum, train_head, exact_weight_grad  # noqa: F401
 from .attn import attention, attention_seq, attn_draws, attn_grad, perturbed_outputs  # noqa: F401
+from .exact import distill, exact_attention, token_logprobs  # noqa: F401

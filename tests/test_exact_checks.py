@@ -1,0 +1,158 @@
+"""The binding and the C-ABI refuse bad calls of the exact losses and attention
+before anything reaches a kernel (no GPU)."""
+import ctypes
+
+import pytest
+import torch
+
+import zeroth_order_transformer_dust_b200 as dust
+from zeroth_order_transformer_dust_b200 import build
+
+f32, bf16, i32 = torch.float32, torch.bfloat16, torch.int32
+
+
+def _t(*shape, dtype=f32):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+class _FakeLib:
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        if not name.startswith("dust_"):
+            raise AttributeError(name)
+
+        def fn(*args):
+            self.calls.append((name, args))
+            return 0
+        return fn
+
+
+def _fake_context():
+    c = dust.Context.__new__(dust.Context)
+    c._L = _FakeLib()
+    c.device = None                       # outputs live in host memory here
+    c._h = ctypes.c_void_p(1)
+    c._stream = None
+    c._bind_stream = lambda: None
+    c._dev = c._cuda = lambda t, name: t  # host tensors stand in for device ones
+    return c
+
+
+def _value(arg):
+    return arg.value if isinstance(arg, ctypes.c_void_p) else arg
+
+
+def test_row_strides():
+    assert dust._row_stride(_t(4, 6), "x") == 6
+    assert dust._row_stride(_t(4, 9)[:, 2:8], "x") == 9
+    assert dust._row_stride(_t(1, 6).expand(1, 6), "x") == 6
+    for bad in (_t(6, 4).t(), _t(4, 12)[:, ::2], _t(1, 6).expand(4, 6), _t(24)):
+        with pytest.raises(ValueError):
+            dust._row_stride(bad, "x")
+
+
+def test_logprobs_call():
+    c = _fake_context()
+    Z, tok = _t(5, 40)[:, 3:33], _t(5, dtype=i32)
+    out = c.token_logprobs(Z, tok, top=4)
+    (name, a), = c._L.calls
+    assert name == "dust_token_logprobs"
+    assert a[1:4] == (5, 30, dust.DUST_F32) and a[5] == 40 and a[7] == 4 and a[12] == 0
+    assert _value(a[4]) == Z.data_ptr() and _value(a[6]) == tok.data_ptr()
+    assert [(k, tuple(v.shape), v.dtype) for k, v in out.items()] == [
+        ("logp", (5,), f32), ("entropy", (5,), f32), ("top_ids", (5, 4), i32),
+        ("top_logp", (5, 4), f32)]
+    out = c.token_logprobs(Z.to(bf16), want_entropy=False, top=1, asynchronous=True)
+    a = c._L.calls[-1][1]
+    assert a[3] == dust.DUST_BF16 and a[6] is None and a[8] is None and a[9] is None
+    assert a[12] == dust.FLAG_ASYNC and set(out) == {"top_ids", "top_logp"}
+    n = len(c._L.calls)
+    for kw in (dict(top=31), dict(top=-1), dict(top=2, out={"top_ids": _t(5, 2)}),
+               dict(top=2, out={"top_ids": _t(5, 3, dtype=i32)}), dict(out={"logp": _t(10)[::2]})):
+        with pytest.raises(ValueError):
+            c.token_logprobs(Z, tok, **kw)
+    with pytest.raises(ValueError):
+        c.token_logprobs(Z, _t(4, dtype=i32))
+    with pytest.raises(TypeError):
+        c.token_logprobs(Z.double(), tok)
+    assert len(c._L.calls) == n
+
+
+def test_distill_call():
+    c = _fake_context()
+    Z, ids, vals = _t(5, 40, dtype=bf16)[:, :30], _t(5, 7, dtype=i32), _t(5, 7)
+    out = c.distill(Z, ids, vals, temperature=2.0, weights=_t(5))
+    (name, a), = c._L.calls
+    assert name == "dust_distill" and a[1:4] == (5, 30, dust.DUST_BF16)
+    assert a[5] == 40 and a[8] == 7 and a[9] == 2.0 and a[13] == 40
+    assert out["dZ"].stride(0) == 40 and tuple(out["dZ"].shape) == (5, 30)
+    assert out["dZ"].dtype == bf16 and tuple(out["loss"].shape) == (5,)
+    dst = _t(5, 64, dtype=bf16)[:, 1:31]
+    assert c.distill(Z, ids, vals, out={"dZ": dst})["dZ"] is dst
+    assert c._L.calls[-1][1][13] == 64
+    out = c.distill(Z, ids, vals, want_grad=False)
+    assert set(out) == {"loss"} and c._L.calls[-1][1][12] is None
+    n = len(c._L.calls)
+    for bad in (dict(weights=_t(4)), dict(out={"dZ": _t(5, 30)}), dict(out={"loss": _t(6)}),
+                dict(out={"dZ": _t(30, 5, dtype=bf16).t()})):
+        with pytest.raises(ValueError):
+            c.distill(Z, ids, vals, **bad)
+    for args in ((Z, ids, _t(5, 6)), (Z, ids[:4], vals)):
+        with pytest.raises(ValueError):
+            c.distill(*args)
+    for args in ((Z, ids.long(), vals), (Z, ids, vals.double())):
+        with pytest.raises(TypeError):
+            c.distill(*args)
+    assert len(c._L.calls) == n
+
+
+def test_attention_calls():
+    c = _fake_context()
+    T, H, G, dh = 12, 4, 2, 64
+    qkv = _t(T, (H + 2 * G) * dh, dtype=bf16)
+    q, k, v = qkv.split([H * dh, G * dh, G * dh], 1)
+    cu = torch.tensor([0, 5, 12], dtype=i32)
+    f = c.attn_forward(q, k, v, n_heads=H, n_kv_heads=G, cu_seqlens=cu, max_len=7, scale=0.5)
+    name, a = c._L.calls[-1]
+    d = a[1]._obj
+    assert name == "dust_attn_forward"
+    assert (d.T, d.n_seqs, d.max_len, d.n_heads, d.n_kv_heads, d.head_dim, d.dtype, d.scale) == (
+        T, 2, 7, H, G, dh, dust.DUST_BF16, 0.5)
+    assert (d.ldq, d.ldk, d.ldv, d.ldo) == (512, 512, 512, 256) and d.cu_seqlens == cu.data_ptr()
+    assert tuple(f["O"].shape) == (T, H * dh) and tuple(f["lse"].shape) == (T, H)
+    g = c.attn_backward(q, k, v, f["O"], f["lse"], _t(T, H * dh, dtype=bf16), n_heads=H,
+                        n_kv_heads=G, seq_len=6, asynchronous=True)
+    name, a = c._L.calls[-1]
+    d = a[1]._obj
+    assert name == "dust_attn_backward" and len(a) == 12
+    assert (d.n_seqs, d.max_len, d.scale, d.flags, d.cu_seqlens) == (2, 6, 0.0, 2, None)
+    assert {n: tuple(x.shape) for n, x in g.items()} == {
+        "dQ": (T, 256), "dK": (T, 128), "dV": (T, 128)}
+    n = len(c._L.calls)
+    for kw in (dict(n_heads=3), dict(n_heads=H), dict(n_heads=H, n_kv_heads=G, seq_len=5),
+               dict(n_heads=H, n_kv_heads=G, scale=0.0),
+               dict(n_heads=H, n_kv_heads=G, seq_len=6, cu_seqlens=cu),
+               dict(n_heads=H, n_kv_heads=G, seq_len=6, max_len=5),
+               dict(n_heads=H, n_kv_heads=G, out={"O": _t(T, 256)})):
+        with pytest.raises(ValueError):
+            c.attn_forward(q, k, v, **kw)
+    with pytest.raises(TypeError):
+        c.attn_forward(q, k.float(), v, n_heads=H, n_kv_heads=G)
+    with pytest.raises(TypeError):
+        c.attn_forward(q, k, v, n_heads=H, n_kv_heads=G, cu_seqlens=cu.long())
+    assert len(c._L.calls) == n
+
+
+def test_null_contexts_and_struct_layout():
+    build.build()
+    L = dust.load_library()
+    assert L.dust_token_logprobs(None, 1, 1, 0, None, 1, None, 0, None, None, None, None, 0) == 1
+    assert L.dust_distill(None, 1, 1, 0, None, 1, None, None, 1, 1.0, None, None, None, 1, 0) == 1
+    d = dust.DustAttnDims()
+    assert L.dust_attn_forward(None, ctypes.byref(d), *[None] * 5) == 1
+    assert L.dust_attn_backward(None, ctypes.byref(d), *[None] * 10) == 1
+    # int64, pointer, int32 x6, float, uint32, int64 x8
+    assert ctypes.sizeof(d) == 112 and dust.DustAttnDims.ldq.offset == 48
+    assert dust.DustAttnDims.scale.offset == 40

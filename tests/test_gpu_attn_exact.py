@@ -1,0 +1,275 @@
+"""Exact causal attention and its gradients on the GPU against the fp64 oracle.
+
+Tolerances, elementwise and from the arithmetic. fp32 tensors: a score is a sum
+of d_h products (relative error at most d_h 2^-24 of the sum of their sizes,
+far less in practice) and an exponential turns its absolute error into a
+relative one; everything after is sums of such terms. F32 = 2e-5 of the sum of
+the terms' sizes covers scores up to ~30. bf16 tensors add half a step (2^-8
+relative) wherever the kernels round: the probabilities p and ds that enter a
+product, the output o that delta = <o, e> is formed from, and the result.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import zeroth_order_transformer_dust_b200 as dust
+from _util import np64
+
+pytestmark = pytest.mark.gpu
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+F32 = 2e-5
+HALF = {"f32": 0.0, "bf16": 2.0 ** -8}
+
+
+@pytest.fixture(scope="module")
+def ctx(cuda_ok):
+    return dust.Context(0)
+
+
+def _inputs(T, heads, kv, dh, dtype, seed, fused=False, sd=1.0):
+    gen = torch.Generator().manual_seed(seed)
+    r = lambda *s: (sd * torch.randn(*s, generator=gen)).to(DT[dtype]).cuda()  # noqa: E731
+    if fused:
+        q, k, v = r(T, (heads + 2 * kv) * dh).split([heads * dh, kv * dh, kv * dh], 1)
+    else:
+        q, k, v = r(T, heads * dh), r(T, kv * dh), r(T, kv * dh)
+    return q, k, v, r(T, heads * dh)
+
+
+def _sizes(Q, K, V, E, O, cu, heads, kv, scale):
+    """Sums of the sizes of the terms behind every output: {name: (of all
+    terms, of the terms that bf16 kernels round)}."""
+    Q, K, V, E, O = (np64(x) for x in (Q, K, V, E, O))
+    dh = Q.shape[1] // heads
+    grp = heads // kv
+    z = {n: np.zeros(x.shape) for n, x in (("O", Q), ("dQ", Q), ("dK", K), ("dV", K))}
+    rnd = {n: x.copy() for n, x in z.items()}
+    for a, b in zip(cu[:-1], cu[1:]):
+        n = b - a
+        low = np.tril(np.ones((n, n), dtype=bool))
+        for h in range(heads):
+            c, g = slice(h * dh, h * dh + dh), slice(h // grp * dh, h // grp * dh + dh)
+            q, k, v, e, o = Q[a:b, c], K[a:b, g], V[a:b, g], E[a:b, c], O[a:b, c]
+            if n == 0:
+                continue
+            s = np.where(low, scale * q @ k.T, -np.inf)
+            p = np.exp(s - s.max(1, keepdims=True))
+            p /= p.sum(1, keepdims=True)
+            z["O"][a:b, c] += p @ np.abs(v)
+            rnd["O"][a:b, c] += p @ np.abs(v)
+            dl = np.abs(o * e).sum(1, keepdims=True)
+            big = p * (np.abs(e) @ np.abs(v).T + dl)
+            ds = np.abs(p * (e @ v.T - (o * e).sum(1, keepdims=True))) + p * dl
+            z["dQ"][a:b, c] += scale * big @ np.abs(k)
+            rnd["dQ"][a:b, c] += scale * ds @ np.abs(k)
+            z["dK"][a:b, g] += scale * big.T @ np.abs(q)
+            rnd["dK"][a:b, g] += scale * ds.T @ np.abs(q)
+            z["dV"][a:b, g] += p.T @ np.abs(e)
+            rnd["dV"][a:b, g] += p.T @ np.abs(e)
+    return z, rnd
+
+
+def _check(ctx, lengths, heads, kv, dh, dtype, fused=False, scale=None, sd=1.0, first=0, tail=0,
+           **kw):
+    cu = first + np.concatenate([[0], np.cumsum(lengths)]).astype(np.int64)
+    T = int(cu[-1]) + tail
+    q, k, v, e = _inputs(T, heads, kv, dh, dtype, seed=T + dh, fused=fused, sd=sd)
+    outside = np.ones(T, dtype=bool)
+    outside[first:cu[-1]] = False
+    for x in (q, k, v, e):          # rows of no sequence are not read
+        x[torch.from_numpy(outside).cuda()] = float("nan")
+    shape = dict(n_heads=heads, n_kv_heads=kv, scale=scale, **kw)
+    if "seq_len" not in kw:
+        shape.update(cu_seqlens=torch.from_numpy(cu.astype(np.int32)).cuda(),
+                     max_len=max(1, max(lengths)))
+    fwd = ctx.attn_forward(q, k, v, out={
+        "O": torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda"),
+        "lse": torch.full((T, heads), 7.0, device="cuda")}, **shape)
+    bwd = ctx.attn_backward(q, k, v, fwd["O"], fwd["lse"], e, out={
+        n: torch.full(x.shape, 7.0, dtype=x.dtype, device="cuda")
+        for n, x in (("dQ", q), ("dK", k), ("dV", v))}, **shape)
+    ref = oracle.exact_attention(np64(q), np64(k), np64(v), cu, heads, kv, scale, E=np64(e))
+    sc = dh ** -0.5 if scale is None else scale
+    z, rnd = _sizes(q, k, v, e, fwd["O"], cu, heads, kv, sc)
+    got = {n: np64(x) for n, x in {**fwd, **bwd}.items()}
+    inside = ~outside
+    for name in ("O", "dQ", "dK", "dV"):
+        tol = F32 * z[name] + HALF[dtype] * (rnd[name] + np.abs(ref[name])) + 1e-30
+        err = np.abs(got[name] - ref[name])
+        assert np.all(err[inside] <= tol[inside]), (name, np.max((err / tol)[inside]))
+    err = np.abs(got["lse"] - ref["lse"])[inside]
+    assert np.all(err <= F32 * (1 + np.abs(ref["lse"][inside])))
+    for name, x in got.items():     # left as they were
+        assert (x[outside] == 7.0).all(), name
+
+
+CASES = [
+    ([1], 1, 1), ([2, 1, 1], 2, 1), ([63], 1, 1), ([64, 65], 2, 2), ([127, 128, 129], 1, 1),
+    ([5, 0, 200, 1], 4, 2), ([300], 8, 1), ([257, 130], 3, 3),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dh", [32, 64, 128])
+@pytest.mark.parametrize("lengths,heads,kv", CASES)
+def test_packed_sequences(ctx, dtype, dh, lengths, heads, kv):
+    _check(ctx, lengths, heads, kv, dh, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dh", [32, 64, 128])
+def test_slices_of_a_fused_projection_with_rows_of_no_sequence(ctx, dtype, dh):
+    # NaN rows in front of the first and behind the last sequence
+    _check(ctx, [70, 0, 190, 3], 4, 2, dh, dtype, fused=True, first=5, tail=77)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_uniform_lengths_scale_and_large_scores(ctx, dtype):
+    _check(ctx, [96, 96, 96], 2, 2, 64, dtype, seq_len=96)
+    _check(ctx, [150], 2, 1, 128, dtype, scale=0.3, sd=1.5)
+    _check(ctx, [600], 1, 1, 64, dtype)
+
+
+def test_unaligned_rows(ctx):
+    # bf16 rows at odd strides and addresses
+    gen = torch.Generator().manual_seed(0)
+    T, heads, dh = 140, 2, 64
+    buf = torch.randn(4, 1 + T * 131, generator=gen).to(torch.bfloat16).cuda()
+    q, k, v, e = (b[1:].view(T, 131)[:, :128] for b in buf)
+    a = ctx.attn_forward(q, k, v, n_heads=heads)
+    b = ctx.attn_forward(*(x.contiguous() for x in (q, k, v)), n_heads=heads)
+    torch.testing.assert_close(a["O"].float(), b["O"].float(), rtol=2e-2, atol=2e-2)
+    ga = ctx.attn_backward(q, k, v, b["O"], b["lse"], e, n_heads=heads)
+    gb = ctx.attn_backward(*(x.contiguous() for x in (q, k, v)), b["O"], b["lse"],
+                           e.contiguous(), n_heads=heads)
+    for name in ga:
+        torch.testing.assert_close(ga[name].float(), gb[name].float(), rtol=2e-2, atol=4e-2)
+
+
+def test_gradients_into_slices_of_one_tensor(ctx):
+    T, heads, kv, dh = 100, 4, 2, 64
+    q, k, v, e = _inputs(T, heads, kv, dh, "bf16", 3)
+    f = ctx.attn_forward(q, k, v, n_heads=heads, n_kv_heads=kv)
+    ref = ctx.attn_backward(q, k, v, f["O"], f["lse"], e, n_heads=heads, n_kv_heads=kv)
+    fused = torch.zeros(T, (heads + 2 * kv) * dh, dtype=torch.bfloat16, device="cuda")
+    dq, dk, dv = fused.split([heads * dh, kv * dh, kv * dh], 1)
+    ctx.attn_backward(q, k, v, f["O"], f["lse"], e, n_heads=heads, n_kv_heads=kv,
+                      out={"dQ": dq, "dK": dk, "dV": dv})
+    assert torch.equal(dq, ref["dQ"]) and torch.equal(dk, ref["dK"]) and torch.equal(dv, ref["dV"])
+
+
+def test_gradient_against_differences(ctx):
+    # d/dx of sum <o, e> in fp32: rounding of the sum (~1e-4) over 2h and the
+    # third derivative's h^2 stay below 1e-2 for h = 0.05
+    T, dh, h = 40, 32, 0.05
+    q, k, v, e = _inputs(T, 2, 1, dh, "f32", 9)
+    f = ctx.attn_forward(q, k, v, n_heads=2, n_kv_heads=1)
+    g = ctx.attn_backward(q, k, v, f["O"], f["lse"], e, n_heads=2, n_kv_heads=1)
+    for x, name, at in ((q, "dQ", (7, 3)), (k, "dK", (12, 1)), (v, "dV", (0, 31))):
+        y = []
+        for s in (h, -2 * h, h):
+            x[at] += s
+            o = ctx.attn_forward(q, k, v, n_heads=2, n_kv_heads=1)["O"]
+            y.append(float((o.double() * e.double()).sum()))
+        assert abs((y[0] - y[1]) / (2 * h) - float(g[name][at])) < 1e-2
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_repeatable_in_a_graph_and_on_another_stream(ctx, dtype):
+    q, k, v, e = _inputs(333, 4, 2, 64, dtype, 5)
+    cu = torch.tensor([0, 200, 333], dtype=torch.int32, device="cuda")
+    kw = dict(n_heads=4, n_kv_heads=2, cu_seqlens=cu, max_len=200)
+    f = ctx.attn_forward(q, k, v, **kw)
+    want = {**f, **ctx.attn_backward(q, k, v, f["O"], f["lse"], e, **kw)}
+    again = ctx.attn_backward(q, k, v, f["O"], f["lse"], e, **kw)
+    for n in again:
+        assert torch.equal(again[n], want[n])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = dust.Context(0, stream=side)
+    got = other.attn_backward(q, k, v, f["O"], f["lse"], e, **kw)
+    side.synchronize()
+    for n in again:
+        assert torch.equal(got[n], want[n])
+    other.close()
+    # two graphs of one context, replayed at the same time on two streams
+    graphs, outs = [], []
+    for _ in range(2):
+        out = {n: torch.zeros_like(x) for n, x in want.items()}
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ff = {n: out[n] for n in ("O", "lse")}
+            ctx.attn_forward(q, k, v, out=ff, asynchronous=True, **kw)
+            ctx.attn_backward(q, k, v, out["O"], out["lse"], e, asynchronous=True,
+                              out={n: out[n] for n in ("dQ", "dK", "dV")}, **kw)
+        graphs.append(g)
+        outs.append(out)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for out in outs:
+        for n in want:
+            assert torch.equal(out[n], want[n]), n
+    ctx.check()
+
+
+def test_bad_offsets_are_reported_and_skipped(ctx):
+    q, k, v, e = _inputs(100, 2, 2, 64, "bf16", 1)
+    for cu, max_len in (([0, 40, 30, 100], 64), ([0, 40, 101], 64), ([-1, 40, 100], 64),
+                        ([0, 70, 100], 64)):
+        cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        with pytest.raises(dust.DustError) as err:
+            ctx.attn_forward(q, k, v, n_heads=2, cu_seqlens=cu, max_len=max_len)
+        assert err.value.status == 4
+    f = ctx.attn_forward(q, k, v, n_heads=2)
+    with pytest.raises(dust.DustError) as err:
+        ctx.attn_backward(q, k, v, f["O"], f["lse"], e, n_heads=2,
+                          cu_seqlens=torch.tensor([0, 200], dtype=torch.int32, device="cuda"))
+    assert err.value.status == 4
+
+
+def test_refusals(ctx):
+    q, k, v, e = _inputs(24, 4, 2, 64, "bf16", 1)
+    ok = dict(n_heads=4, n_kv_heads=2)
+    f = ctx.attn_forward(q, k, v, **ok)
+    for bad in (dict(n_heads=3, n_kv_heads=1), dict(n_heads=4, n_kv_heads=3), dict(n_heads=4),
+                dict(ok, seq_len=7), dict(ok, scale=0.0), dict(ok, scale=-1.0),
+                dict(ok, seq_len=24, cu_seqlens=torch.zeros(2, dtype=torch.int32, device="cuda"))):
+        with pytest.raises(ValueError):
+            ctx.attn_forward(q, k, v, **bad)
+    for bad in (dict(ok, scale=float("inf")), dict(n_heads=16, n_kv_heads=8)):  # 16-wide heads
+        with pytest.raises(dust.DustError) as err:
+            ctx.attn_forward(q, k, v, **bad)
+        assert err.value.status == 1
+    with pytest.raises(TypeError):
+        ctx.attn_forward(q, k.float(), v, **ok)
+    with pytest.raises(TypeError):
+        ctx.attn_backward(q, k, v, f["O"].float(), f["lse"], e, **ok)
+    with pytest.raises(ValueError):
+        ctx.attn_backward(q, k, v, f["O"], f["lse"][:, :2], e, **ok)
+    with pytest.raises(TypeError):
+        ctx.attn_forward(q, k, v, cu_seqlens=torch.zeros(2, dtype=torch.int64, device="cuda"), **ok)
+    empty = ctx.attn_forward(q[:0], k[:0], v[:0], **ok)
+    assert empty["O"].shape == (0, 256)
+
+
+def test_the_estimator_converges_to_the_exact_gradient(ctx):
+    # attn_grad's g for each projection against attn_backward, as a user would
+    # compare them: with K draws of D = 64 channels the estimate's cosine with
+    # the gradient is about 1 / sqrt(1 + (D + 1) / K)
+    T, L, heads, dh, K = 96, 48, 1, 64, 16384
+    q, k, v, e = _inputs(T, heads, heads, dh, "f32", 21)
+    x = torch.randn(T, 32, device="cuda")
+    f = ctx.attn_forward(q, k, v, n_heads=heads, seq_len=L)
+    ex = ctx.attn_backward(q, k, v, f["O"], f["lse"], e, n_heads=heads, seq_len=L)
+    for which, name in (("q", "dQ"), ("k", "dK"), ("v", "dV")):
+        g = ctx.attn_grad(x, q, k, v, e, seq_len=L, n_heads=heads, which=which, K=K, sigma=1e-3,
+                          want_G=False, want_g=True)["g"]
+        cos = torch.nn.functional.cosine_similarity(g.flatten().double(),
+                                                    ex[name].flatten().double(), dim=0)
+        assert float(cos) > 0.99, which

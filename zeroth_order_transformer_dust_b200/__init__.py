@@ -37,7 +37,8 @@ EXPORTS = ("dust_create", "dust_set_stream", "dust_destroy", "dust_last_error",
            "dust_debug_gauss_tab_scalar",
            "dust_head_grad_noalloc", "dust_debug_bm_radius", "dust_debug_bm_angle",
            "dust_attn_grad",
-           "dust_sgd_momentum", "dust_mlp_down_grad", "dust_attn_out_grad")
+           "dust_sgd_momentum", "dust_mlp_down_grad", "dust_attn_out_grad",
+           "dust_token_logprobs", "dust_distill", "dust_attn_forward", "dust_attn_backward")
 
 
 class DustParams(ctypes.Structure):
@@ -56,6 +57,17 @@ class DustAttnShape(ctypes.Structure):
 
 
 ATTN_WHICH = {"q": 0, "k": 1, "v": 2}
+
+
+class DustAttnDims(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("cu_seqlens", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int32), ("max_len", ctypes.c_int32),
+                ("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("flags", ctypes.c_uint32),
+                ("ldq", ctypes.c_int64), ("ldk", ctypes.c_int64), ("ldv", ctypes.c_int64),
+                ("ldo", ctypes.c_int64), ("lde", ctypes.c_int64), ("lddq", ctypes.c_int64),
+                ("lddk", ctypes.c_int64), ("lddv", ctypes.c_int64)]
 
 
 class DustError(RuntimeError):
@@ -112,6 +124,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             "dust_debug_bm_radius": (I32, [P, I32, ctypes.c_float, P]),
             "dust_debug_bm_angle": (I32, [P, I32, P]),
             "dust_sgd_momentum": (I32, [P, I64, ctypes.c_float, ctypes.c_float, P, P, P, P]),
+            "dust_token_logprobs": (I32, [P, I64, I64, I32, P, I64, P, I32, P, P, P, P, U32]),
+            "dust_distill": (I32, [P, I64, I64, I32, P, I64, P, P, I32, ctypes.c_float, P, P, P,
+                                   I64, U32]),
+            "dust_attn_forward": (I32, [P, ctypes.POINTER(DustAttnDims), P, P, P, P, P]),
+            "dust_attn_backward": (I32, [P, ctypes.POINTER(DustAttnDims)] + [P] * 10),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -227,6 +244,100 @@ def _attn_shapes(X, Q, K_cache, V_cache, E, n_heads):
     if n_heads < 1 or D % n_heads:
         raise ValueError("the width of Q must be a positive multiple of n_heads")
     return T, d, D
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between the rows of a 2-D tensor whose rows are contiguous
+    and do not overlap."""
+    rows, width = _matrix(t, name)
+    ld, step = t.stride()
+    if (width > 1 and step != 1) or (rows > 1 and ld < width):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return max(ld, width) if rows > 1 else width
+
+
+def _check_output(out: dict, key: str, shape, dtype, device: Optional[int], rows: bool = False):
+    """One caller-supplied output: dtype, shape, on cuda:device (None: host
+    memory), contiguous (or, with ``rows``, of contiguous rows)."""
+    t = out.get(key)
+    if t is None:
+        return
+    _shape(t, shape, f"output {key}")
+    if t.dtype != dtype:
+        raise ValueError(f"output {key} must be {str(dtype)[6:]}")
+    if rows:
+        _row_stride(t, f"output {key}")
+    elif not t.is_contiguous():
+        raise ValueError(f"output {key} must be contiguous")
+    if (device is None and t.is_cuda) or (
+            device is not None and not (t.is_cuda and t.device.index == device)):
+        raise ValueError(f"output {key} is on the wrong device")
+
+
+def _logprob_shapes(Z, tokens, top):
+    """(T, V, row stride) of a token_logprobs call."""
+    T, V = _matrix(Z, "Z")
+    if tokens is not None:
+        _shape(tokens, (T,), "tokens")
+        if tokens.dtype != torch.int32:
+            raise TypeError("tokens must be int32")
+    if not 0 <= top <= min(V, 128):
+        raise ValueError("top must lie in [0, min(V, 128)]")
+    return T, V, _row_stride(Z, "Z")
+
+
+def _distill_shapes(Z, teacher_ids, teacher_vals, weights):
+    """(T, V, k, row stride) of a distill call."""
+    T, V = _matrix(Z, "Z")
+    k = _matrix(teacher_ids, "teacher_ids")[1]
+    _shape(teacher_ids, (T, k), "teacher_ids")
+    _shape(teacher_vals, (T, k), "teacher_vals")
+    if teacher_ids.dtype != torch.int32:
+        raise TypeError("teacher_ids must be int32")
+    if teacher_vals.dtype != torch.float32:
+        raise TypeError("teacher_vals must be fp32")
+    if weights is not None:
+        _shape(weights, (T,), "weights")
+        if weights.dtype != torch.float32:
+            raise TypeError("weights must be fp32")
+    return T, V, k, _row_stride(Z, "Z")
+
+
+def _exact_attn_dims(Q, K_cache, V_cache, n_heads, n_kv_heads, seq_len, cu_seqlens, max_len,
+                     scale) -> DustAttnDims:
+    """Sizes of an attn_forward or attn_backward call (strides of Q, K, V set)."""
+    T, D = _matrix(Q, "Q")
+    n_kv_heads = n_heads if n_kv_heads is None else n_kv_heads
+    if n_heads < 1 or D % n_heads:
+        raise ValueError("the width of Q must be a positive multiple of n_heads")
+    if n_kv_heads < 1 or n_heads % n_kv_heads:
+        raise ValueError("n_heads must be a multiple of n_kv_heads")
+    head_dim = D // n_heads
+    for t, n in ((K_cache, "K_cache"), (V_cache, "V_cache")):
+        _shape(t, (T, n_kv_heads * head_dim), n)
+        if t.dtype != Q.dtype:
+            raise TypeError(f"{n} must have Q's dtype")
+    dims = DustAttnDims(T=T, n_heads=n_heads, n_kv_heads=n_kv_heads, head_dim=head_dim,
+                        dtype=_dtype_code(Q), scale=0.0 if scale is None else scale,
+                        ldq=_row_stride(Q, "Q"), ldk=_row_stride(K_cache, "K_cache"),
+                        ldv=_row_stride(V_cache, "V_cache"))
+    if scale is not None and not scale > 0.0:
+        raise ValueError("scale must be > 0")
+    if cu_seqlens is not None:
+        if seq_len is not None:
+            raise ValueError("give seq_len or cu_seqlens, not both")
+        if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise TypeError("cu_seqlens must be a 1-D int32 tensor of n_seqs + 1 offsets")
+        dims.n_seqs = cu_seqlens.numel() - 1
+        dims.max_len = max(T, 1) if max_len is None else max_len
+    else:
+        length = max(T, 1) if seq_len is None else seq_len
+        if length < 1 or T % length:
+            raise ValueError("T must be a multiple of seq_len")
+        if max_len is not None and max_len != length:
+            raise ValueError("max_len goes with cu_seqlens")
+        dims.n_seqs, dims.max_len = T // length, length
+    return dims
 
 
 class Context:
@@ -423,6 +534,156 @@ class Context:
                                            _ptr(out.get("g"))))
         return out
 
+    # -- exact losses and gradients ------------------------------------------------
+    def _cuda(self, t: torch.Tensor, name: str):
+        if not t.is_cuda or t.device.index != self.device:
+            raise ValueError(f"{name} must be on cuda:{self.device}")
+        return t
+
+    def _empty(self, shape, dtype, device) -> torch.Tensor:
+        """Memory for this context's stream (outputs and scratch of a call)."""
+        if self._stream is None:
+            return torch.empty(shape, dtype=dtype, device=device)
+        with torch.cuda.stream(self._stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+    def token_logprobs(self, Z, tokens=None, *, top=0, want_entropy=True, asynchronous=False,
+                       out=None) -> dict:
+        """Scores of the logits Z (T x V, fp32 or bf16, rows may be strided):
+        "logp" (T,) of ``tokens`` (T int32; -1: none, logp 0), "entropy" (T,),
+        and the ``top`` most likely tokens as "top_ids" (T x top int32) and
+        "top_logp" (T x top), likeliest first, equal logits by the lower id.
+        Logits of -inf are masked; alternatives that a row lacks have id -1."""
+        T, V, ld = _logprob_shapes(Z, tokens, top)
+        self._cuda(Z, "Z")
+        if tokens is not None:
+            self._dev(tokens, "tokens")
+        out = dict(out or {})
+        spec = {}
+        if tokens is not None:
+            spec["logp"] = ((T,), torch.float32)
+        if want_entropy:
+            spec["entropy"] = ((T,), torch.float32)
+        if top:
+            spec["top_ids"] = ((T, top), torch.int32)
+            spec["top_logp"] = ((T, top), torch.float32)
+        for key, (shape, dt) in spec.items():
+            if key in out:
+                _check_output(out, key, shape, dt, self.device)
+            else:
+                out[key] = self._empty(shape, dt, Z.device)
+        self._bind_stream()
+        p = [_ptr(out[key]) if key in spec else None
+             for key in ("logp", "entropy", "top_ids", "top_logp")]
+        self._check(self._L.dust_token_logprobs(self._h, T, V, _dtype_code(Z), _ptr(Z), ld,
+                                                _ptr(tokens), top, *p,
+                                                FLAG_ASYNC if asynchronous else 0))
+        return out
+
+    def distill(self, Z, teacher_ids, teacher_vals, *, temperature=1.0, weights=None,
+                want_loss=True, want_grad=True, asynchronous=False, out=None) -> dict:
+        """Distillation of the student logits Z (T x V, fp32 or bf16, rows may be
+        strided) from a teacher's kept entries: teacher_ids (T x k int32, -1:
+        none) and teacher_vals (T x k fp32 logits or log probabilities), for
+        instance token_logprobs' alternatives of the teacher. "loss" (T,) is
+        temperature^2 KL(teacher || student); "dZ" (T x V, Z's dtype and row
+        stride) the gradient of sum_t weights_t loss_t (weights: T fp32,
+        default 1). Rows of weight 0 or without an entry give zeros.
+        out={"dZ": Z} writes the gradient over the logits."""
+        T, V, k, ld = _distill_shapes(Z, teacher_ids, teacher_vals, weights)
+        self._cuda(Z, "Z")
+        self._dev(teacher_ids, "teacher_ids"), self._dev(teacher_vals, "teacher_vals")
+        if weights is not None:
+            self._dev(weights, "weights")
+        out = dict(out or {})
+        loss = dZ = None
+        ldg = V
+        if want_loss:
+            _check_output(out, "loss", (T,), torch.float32, self.device)
+            if "loss" not in out:
+                out["loss"] = self._empty((T,), torch.float32, Z.device)
+            loss = out["loss"]
+        if want_grad:
+            _check_output(out, "dZ", (T, V), Z.dtype, self.device, rows=True)
+            if "dZ" not in out:
+                out["dZ"] = self._empty((T, ld), Z.dtype, Z.device)[:, :V]
+            dZ = out["dZ"]
+            ldg = _row_stride(dZ, "output dZ")
+        self._bind_stream()
+        self._check(self._L.dust_distill(self._h, T, V, _dtype_code(Z), _ptr(Z), ld,
+                                         _ptr(teacher_ids), _ptr(teacher_vals), k,
+                                         float(temperature), _ptr(weights), _ptr(loss), _ptr(dZ),
+                                         ldg, FLAG_ASYNC if asynchronous else 0))
+        return out
+
+    def attn_forward(self, Q, K_cache, V_cache, *, n_heads, n_kv_heads=None, seq_len=None,
+                     cu_seqlens=None, max_len=None, scale=None, asynchronous=False,
+                     out=None) -> dict:
+        """Causal attention of packed sequences: "O" (like Q) and "lse" (T x
+        n_heads fp32). Q is T x (n_heads d_h), K_cache and V_cache T x
+        (n_kv_heads d_h), fp32 or bf16, d_h 32, 64 or 128; rows may be strided.
+        The sequences are of ``seq_len`` rows each, or lie between the offsets
+        ``cu_seqlens`` (device int32; ``max_len`` bounds their length, by default
+        T), or are one. ``scale`` defaults to 1 / sqrt(d_h)."""
+        dims = _exact_attn_dims(Q, K_cache, V_cache, n_heads, n_kv_heads, seq_len, cu_seqlens,
+                                max_len, scale)
+        for t, n in ((Q, "Q"), (K_cache, "K_cache"), (V_cache, "V_cache")):
+            self._cuda(t, n)
+        out = dict(out or {})
+        T = dims.T
+        _check_output(out, "O", tuple(Q.shape), Q.dtype, self.device, rows=True)
+        _check_output(out, "lse", (T, n_heads), torch.float32, self.device)
+        if "O" not in out:
+            out["O"] = self._empty(tuple(Q.shape), Q.dtype, Q.device)
+        if "lse" not in out:
+            out["lse"] = self._empty((T, n_heads), torch.float32, Q.device)
+        dims.ldo = _row_stride(out["O"], "output O")
+        self._attn_call(dims, cu_seqlens, asynchronous)
+        self._check(self._L.dust_attn_forward(self._h, ctypes.byref(dims), _ptr(Q), _ptr(K_cache),
+                                              _ptr(V_cache), _ptr(out["O"]), _ptr(out["lse"])))
+        return out
+
+    def attn_backward(self, Q, K_cache, V_cache, O, lse, E, *, n_heads, n_kv_heads=None,
+                      seq_len=None, cu_seqlens=None, max_len=None, scale=None,
+                      asynchronous=False, out=None) -> dict:
+        """Gradients "dQ", "dK", "dV" of sum_t <o_t, e_t> for the error signal E
+        (like Q) at the attention output: what attn_grad estimates without
+        backprop, exactly. O and lse are attn_forward's; the other arguments as
+        there. The gradients have the dtype of the inputs; dK and dV sum over
+        the heads that share a key/value head."""
+        dims = _exact_attn_dims(Q, K_cache, V_cache, n_heads, n_kv_heads, seq_len, cu_seqlens,
+                                max_len, scale)
+        for t, n in ((O, "O"), (E, "E")):
+            _shape(t, tuple(Q.shape), n)
+            if t.dtype != Q.dtype:
+                raise TypeError(f"{n} must have Q's dtype")
+        _shape(lse, (dims.T, n_heads), "lse")
+        if lse.dtype != torch.float32:
+            raise TypeError("lse must be fp32")
+        for t, n in ((Q, "Q"), (K_cache, "K_cache"), (V_cache, "V_cache"), (O, "O"), (E, "E")):
+            self._cuda(t, n)
+        self._dev(lse, "lse")
+        dims.ldo, dims.lde = _row_stride(O, "O"), _row_stride(E, "E")
+        out = dict(out or {})
+        for key, like in (("dQ", Q), ("dK", K_cache), ("dV", V_cache)):
+            _check_output(out, key, tuple(like.shape), Q.dtype, self.device, rows=True)
+            if key not in out:
+                out[key] = self._empty(tuple(like.shape), Q.dtype, Q.device)
+        dims.lddq, dims.lddk, dims.lddv = (_row_stride(out[k], f"output {k}")
+                                           for k in ("dQ", "dK", "dV"))
+        delta = self._empty((dims.T, n_heads), torch.float32, Q.device)
+        self._attn_call(dims, cu_seqlens, asynchronous)
+        self._check(self._L.dust_attn_backward(
+            self._h, ctypes.byref(dims), _ptr(Q), _ptr(K_cache), _ptr(V_cache), _ptr(O), _ptr(lse),
+            _ptr(E), _ptr(out["dQ"]), _ptr(out["dK"]), _ptr(out["dV"]), _ptr(delta)))
+        return out
+
+    def _attn_call(self, dims: DustAttnDims, cu_seqlens, asynchronous: bool):
+        if cu_seqlens is not None:
+            dims.cu_seqlens = self._dev(cu_seqlens, "cu_seqlens").data_ptr()
+        dims.flags = FLAG_ASYNC if asynchronous else 0
+        self._bind_stream()
+
     # -- instrumentation -------------------------------------------------------------
     def set_stage_timing(self, enable: bool = True):
         self._check(self._L.dust_set_stage_timing(self._h, 1 if enable else 0))
@@ -550,3 +811,19 @@ def mlp_grad(X, W_up, W_down, W_head, targets, **kw) -> dict:
 
 def attn_grad(X, Q, K_cache, V_cache, E, **kw) -> dict:
     return context(X.device.index).attn_grad(X, Q, K_cache, V_cache, E, **kw)
+
+
+def token_logprobs(Z, tokens=None, **kw) -> dict:
+    return context(Z.device.index).token_logprobs(Z, tokens, **kw)
+
+
+def distill(Z, teacher_ids, teacher_vals, **kw) -> dict:
+    return context(Z.device.index).distill(Z, teacher_ids, teacher_vals, **kw)
+
+
+def attn_forward(Q, K_cache, V_cache, **kw) -> dict:
+    return context(Q.device.index).attn_forward(Q, K_cache, V_cache, **kw)
+
+
+def attn_backward(Q, K_cache, V_cache, O, lse, E, **kw) -> dict:
+    return context(Q.device.index).attn_backward(Q, K_cache, V_cache, O, lse, E, **kw)

@@ -300,6 +300,65 @@ dust_status full_split_draws(dust_ctx* ctx, const dust_params& p, const FullOneP
   return DUST_OK;
 }
 
+// Logits of the vocabulary losses: T x V rows with stride ldz.
+dust_status check_logits(dust_ctx* ctx, int64_t T, int64_t V, int32_t dtype, const void* Z,
+                         int64_t ldz) {
+  if (dtype != DUST_F32 && dtype != DUST_BF16)
+    return fail(ctx, DUST_ERR_ARG, "dtype must be DUST_F32 or DUST_BF16");
+  if (T < 0 || T > (1LL << 27)) return fail(ctx, DUST_ERR_ARG, "T must lie in [0, 2^27]");
+  if (V < 1 || V > 0x7fffffffLL) return fail(ctx, DUST_ERR_ARG, "V must lie in [1, 2^31)");
+  if (T > 1 && (ldz < V || ldz > (1LL << 40)))
+    return fail(ctx, DUST_ERR_ARG, "ldz must lie in [V, 2^40]");
+  if (T > 0 && !Z) return fail(ctx, DUST_ERR_ARG, "Z must be non-NULL");
+  if (!aligned(Z, elem_size(dtype))) return fail(ctx, DUST_ERR_ARG, "Z must be aligned to its elements");
+  return DUST_OK;
+}
+
+// Sizes of the exact attention calls, into *a.
+dust_status check_attn_dims(dust_ctx* ctx, const dust_attn_dims* d, AttnArgs* a) {
+  if (!d) return fail(ctx, DUST_ERR_ARG, "dims is NULL");
+  if (d->dtype != DUST_F32 && d->dtype != DUST_BF16)
+    return fail(ctx, DUST_ERR_ARG, "dtype must be DUST_F32 or DUST_BF16");
+  if (d->head_dim != 32 && d->head_dim != 64 && d->head_dim != 128)
+    return fail(ctx, DUST_ERR_ARG, "head_dim must be 32, 64 or 128");
+  if (d->n_kv_heads < 1 || d->n_heads < 1 || d->n_heads > 65535 || d->n_heads % d->n_kv_heads)
+    return fail(ctx, DUST_ERR_ARG,
+                "n_heads must lie in [1, 65535] and be a multiple of n_kv_heads >= 1");
+  if (d->n_seqs < 0 || d->n_seqs > 65535)
+    return fail(ctx, DUST_ERR_ARG, "n_seqs must lie in [0, 65535]");
+  if (d->T < 0 || d->T > 0x7fffffffLL) return fail(ctx, DUST_ERR_ARG, "T must lie in [0, 2^31)");
+  if (d->max_len < 1 || d->max_len > (1 << 24))
+    return fail(ctx, DUST_ERR_ARG, "max_len must lie in [1, 2^24]");
+  if (!d->cu_seqlens && (int64_t)d->n_seqs * d->max_len > d->T)
+    return fail(ctx, DUST_ERR_ARG, "n_seqs sequences of max_len rows exceed T");
+  if (!std::isfinite(d->scale) || d->scale < 0.0f)
+    return fail(ctx, DUST_ERR_ARG, "scale must be finite and > 0, or 0 for 1 / sqrt(head_dim)");
+  if (!aligned(d->cu_seqlens, 4)) return fail(ctx, DUST_ERR_ARG, "cu_seqlens must be 4-byte aligned");
+  a->cu = d->cu_seqlens;
+  a->T = d->T;
+  a->n_seqs = d->n_seqs;
+  a->max_len = d->max_len;
+  a->H = d->n_heads;
+  a->Hkv = d->n_kv_heads;
+  a->head_dim = d->head_dim;
+  a->dtype = d->dtype;
+  a->scale = d->scale > 0.0f ? d->scale : 1.0f / std::sqrt((float)d->head_dim);
+  a->ldq = d->ldq; a->ldk = d->ldk; a->ldv = d->ldv; a->ldo = d->ldo; a->lde = d->lde;
+  a->lddq = d->lddq; a->lddk = d->lddk; a->lddv = d->lddv;
+  return DUST_OK;
+}
+
+dust_status check_rows(dust_ctx* ctx, const AttnArgs& a, const char* name, const void* p,
+                       int64_t ld, int64_t width) {
+  if (a.T > 0 && !p) return fail(ctx, DUST_ERR_ARG, "%s must be non-NULL", name);
+  if (!aligned(p, elem_size(a.dtype)))
+    return fail(ctx, DUST_ERR_ARG, "%s must be aligned to its elements", name);
+  if (a.T > 1 && (ld < width || ld > (1LL << 31)))
+    return fail(ctx, DUST_ERR_ARG, "%s's row stride must lie in [%lld, 2^31]", name,
+                (long long)width);
+  return DUST_OK;
+}
+
 // Stage marks: mark(ctx, nullptr) opens a call, mark(ctx, "name") closes the
 // stage that ran since the previous mark.
 void mark(dust_ctx* ctx, const char* name) {
@@ -418,6 +477,9 @@ dust_status dust_check(dust_ctx* ctx) {
   const uint32_t st = *ctx->h_status;
   if (st) DUST_CU(cudaMemsetAsync(ctx->d_status, 0, sizeof(uint32_t), ctx->stream));
   if (st & kStatusBadTarget) return fail(ctx, DUST_ERR_BOUNDS, "a target lies outside [0, V)");
+  if (st & kStatusBadSeq)
+    return fail(ctx, DUST_ERR_BOUNDS,
+                "cu_seqlens must not decrease, leave [0, T] or exceed max_len rows a sequence");
   if (st & kStatusTimeout) return fail(ctx, DUST_ERR_TIMEOUT, "a bounded device wait expired");
   if (st & kStatusRange)
     return fail(ctx, DUST_ERR_UNSUPPORTED,
@@ -998,6 +1060,124 @@ dust_status dust_attn_grad(dust_ctx* ctx, const dust_params* pp, const dust_attn
     mark(ctx, "gw_gemm");
   }
   return finish(ctx, p.flags);
+}
+
+dust_status dust_token_logprobs(dust_ctx* ctx, int64_t T, int64_t V, int32_t dtype, const void* Z,
+                                int64_t ldz, const int32_t* tokens, int32_t top, float* logp_out,
+                                float* entropy_out, int32_t* top_ids_out, float* top_logp_out,
+                                uint32_t flags) {
+  if (!ctx) return DUST_ERR_ARG;
+  DUST_TRY(check_logits(ctx, T, V, dtype, Z, ldz));
+  if (top < 0 || top > kTopLimit || top > V)
+    return fail(ctx, DUST_ERR_ARG, "top must lie in [0, min(V, %d)]", kTopLimit);
+  if (T == 0) return finish(ctx, flags);
+  if ((top > 0) != (top_ids_out != nullptr) || (top > 0) != (top_logp_out != nullptr))
+    return fail(ctx, DUST_ERR_ARG, "top_ids and top_logp are given exactly for top > 0");
+  if ((tokens != nullptr) != (logp_out != nullptr))
+    return fail(ctx, DUST_ERR_ARG, "tokens and logp go together");
+  if (!aligned(tokens, 4) || !aligned(logp_out, 4) || !aligned(entropy_out, 4) ||
+      !aligned(top_ids_out, 4) || !aligned(top_logp_out, 4))
+    return fail(ctx, DUST_ERR_ARG, "tokens and the outputs must be 4-byte aligned");
+  DUST_CU(cudaSetDevice(ctx->device));
+  mark(ctx, nullptr);
+  DUST_CU(launch_token_logprobs(ctx->stream, Z, dtype, T, V, ldz, tokens, top, logp_out,
+                                entropy_out, top_ids_out, top_logp_out, ctx->sm_count,
+                                ctx->d_status));
+  ctx->launches += 1;
+  mark(ctx, "token_logprobs");
+  return finish(ctx, flags);
+}
+
+dust_status dust_distill(dust_ctx* ctx, int64_t T, int64_t V, int32_t dtype, const void* Z,
+                         int64_t ldz, const int32_t* teacher_ids, const float* teacher_vals,
+                         int32_t k, float temperature, const float* weights, float* loss_out,
+                         void* dZ_out, int64_t lddz, uint32_t flags) {
+  if (!ctx) return DUST_ERR_ARG;
+  DUST_TRY(check_logits(ctx, T, V, dtype, Z, ldz));
+  if (k < 1 || k > kTopLimit) return fail(ctx, DUST_ERR_ARG, "k must lie in [1, %d]", kTopLimit);
+  // (the kernels use log2(e) / temperature and temperature^2)
+  if (!(temperature >= 1e-6f) || !(temperature <= 1e6f))
+    return fail(ctx, DUST_ERR_ARG, "temperature must lie in [1e-6, 1e6]");
+  if (T == 0) return finish(ctx, flags);
+  if (!teacher_ids || !teacher_vals)
+    return fail(ctx, DUST_ERR_ARG, "teacher_ids and teacher_vals must be non-NULL");
+  if (!aligned(teacher_ids, 4) || !aligned(teacher_vals, 4) || !aligned(weights, 4) ||
+      !aligned(loss_out, 4))
+    return fail(ctx, DUST_ERR_ARG, "teacher_ids, teacher_vals, weights, loss must be 4-byte aligned");
+  if (dZ_out) {
+    if (!aligned(dZ_out, elem_size(dtype)))
+      return fail(ctx, DUST_ERR_ARG, "dZ must be aligned to its elements");
+    if (T > 1 && (lddz < V || lddz > (1LL << 40))) return fail(ctx, DUST_ERR_ARG, "lddz must lie in [V, 2^40]");
+    const uintptr_t z0 = (uintptr_t)Z, g0 = (uintptr_t)dZ_out, es = elem_size(dtype);
+    const uintptr_t zb = ((uintptr_t)(T - 1) * (uintptr_t)ldz + (uintptr_t)V) * es;
+    const uintptr_t gb = ((uintptr_t)(T - 1) * (uintptr_t)lddz + (uintptr_t)V) * es;
+    const bool same = z0 == g0 && (ldz == lddz || T <= 1);
+    if (!same && z0 < g0 + gb && g0 < z0 + zb)
+      return fail(ctx, DUST_ERR_ARG, "dZ must be Z itself (same row stride) or apart from it");
+  }
+  if (!loss_out && !dZ_out) return fail(ctx, DUST_ERR_ARG, "neither loss nor dZ is asked for");
+  DUST_CU(cudaSetDevice(ctx->device));
+  mark(ctx, nullptr);
+  DUST_CU(launch_distill(ctx->stream, Z, dtype, T, V, ldz, teacher_ids, teacher_vals, k,
+                         temperature, weights, loss_out, dZ_out, lddz, ctx->sm_count,
+                         ctx->d_status));
+  ctx->launches += 1;
+  mark(ctx, "distill");
+  return finish(ctx, flags);
+}
+
+dust_status dust_attn_forward(dust_ctx* ctx, const dust_attn_dims* dims, const void* Q,
+                              const void* Kc, const void* Vc, void* O_out, float* lse_out) {
+  if (!ctx) return DUST_ERR_ARG;
+  AttnArgs a{};
+  DUST_TRY(check_attn_dims(ctx, dims, &a));
+  const int64_t dq = (int64_t)a.H * a.head_dim, dk = (int64_t)a.Hkv * a.head_dim;
+  DUST_TRY(check_rows(ctx, a, "Q", Q, a.ldq, dq));
+  DUST_TRY(check_rows(ctx, a, "K", Kc, a.ldk, dk));
+  DUST_TRY(check_rows(ctx, a, "V", Vc, a.ldv, dk));
+  DUST_TRY(check_rows(ctx, a, "O", O_out, a.ldo, dq));
+  if (a.T > 0 && !lse_out) return fail(ctx, DUST_ERR_ARG, "lse must be non-NULL");
+  if (!aligned(lse_out, 4)) return fail(ctx, DUST_ERR_ARG, "lse must be 4-byte aligned");
+  DUST_CU(cudaSetDevice(ctx->device));
+  if (a.T == 0 || a.n_seqs == 0) return finish(ctx, dims->flags);
+  a.Q = Q; a.K = Kc; a.V = Vc; a.O = O_out; a.lse_out = lse_out;
+  a.status = ctx->d_status;
+  mark(ctx, nullptr);
+  DUST_CU(launch_attn_exact_simt(ctx->stream, a, false));
+  ctx->launches += 1;
+  mark(ctx, "attn_forward");
+  return finish(ctx, dims->flags);
+}
+
+dust_status dust_attn_backward(dust_ctx* ctx, const dust_attn_dims* dims, const void* Q,
+                               const void* Kc, const void* Vc, const void* O, const float* lse,
+                               const void* E, void* dQ_out, void* dK_out, void* dV_out,
+                               float* delta) {
+  if (!ctx) return DUST_ERR_ARG;
+  AttnArgs a{};
+  DUST_TRY(check_attn_dims(ctx, dims, &a));
+  const int64_t dq = (int64_t)a.H * a.head_dim, dk = (int64_t)a.Hkv * a.head_dim;
+  DUST_TRY(check_rows(ctx, a, "Q", Q, a.ldq, dq));
+  DUST_TRY(check_rows(ctx, a, "K", Kc, a.ldk, dk));
+  DUST_TRY(check_rows(ctx, a, "V", Vc, a.ldv, dk));
+  DUST_TRY(check_rows(ctx, a, "O", O, a.ldo, dq));
+  DUST_TRY(check_rows(ctx, a, "E", E, a.lde, dq));
+  DUST_TRY(check_rows(ctx, a, "dQ", dQ_out, a.lddq, dq));
+  DUST_TRY(check_rows(ctx, a, "dK", dK_out, a.lddk, dk));
+  DUST_TRY(check_rows(ctx, a, "dV", dV_out, a.lddv, dk));
+  if (a.T > 0 && (!lse || !delta)) return fail(ctx, DUST_ERR_ARG, "lse and delta must be non-NULL");
+  if (!aligned(lse, 4) || !aligned(delta, 4))
+    return fail(ctx, DUST_ERR_ARG, "lse and delta must be 4-byte aligned");
+  DUST_CU(cudaSetDevice(ctx->device));
+  if (a.T == 0 || a.n_seqs == 0) return finish(ctx, dims->flags);
+  a.Q = Q; a.K = Kc; a.V = Vc; a.O_in = O; a.lse = lse; a.E = E;
+  a.dQ = dQ_out; a.dK = dK_out; a.dV = dV_out; a.delta = delta;
+  a.status = ctx->d_status;
+  mark(ctx, nullptr);
+  DUST_CU(launch_attn_exact_simt(ctx->stream, a, true));
+  ctx->launches += 2;
+  mark(ctx, "attn_backward");
+  return finish(ctx, dims->flags);
 }
 
 dust_status dust_set_stage_timing(dust_ctx* ctx, int enable) {

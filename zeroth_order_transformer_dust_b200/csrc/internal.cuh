@@ -16,6 +16,7 @@ enum : uint32_t {
   kStatusBadTarget = 1u << 0,
   kStatusTimeout = 1u << 1,
   kStatusRange = 1u << 2,  // an operand outside the range a kernel's format holds
+  kStatusBadSeq = 1u << 3,  // sequence offsets that decrease or leave [0, T]
 };
 
 struct Buf {
@@ -420,5 +421,50 @@ size_t attn_tc_rows_bytes(int64_t T, int L, int H, int head_dim);
 size_t attn_coef_bytes(int64_t T, int L, int H);
 cudaError_t launch_attn_combine(cudaStream_t st, const float* part, int64_t T, int H, int K,
                                 float* r);
+
+// Log probabilities of given tokens, entropy and the `top` best alternatives
+// of each row of Z (T x V, row stride ld). tokens may be null (then logp too).
+constexpr int kTopLimit = 128;  // alternatives, and a teacher's kept entries, per row
+cudaError_t launch_token_logprobs(cudaStream_t st, const void* Z, int dtype, int64_t T, int64_t V,
+                                  int64_t ld, const int32_t* tokens, int top, float* logp,
+                                  float* entropy, int32_t* top_ids, float* top_logp, int sm_count,
+                                  uint32_t* status);
+// Distillation from a teacher's k kept entries per row (ids and vals T x k):
+// loss (T, may be null) and, when dZ is not null, the gradient of
+// sum_t weights_t loss_t in Z's dtype (row stride ldg; dZ may be Z).
+cudaError_t launch_distill(cudaStream_t st, const void* Z, int dtype, int64_t T, int64_t V,
+                           int64_t ld, const int32_t* ids, const float* vals, int k, float tau,
+                           const float* weights, float* loss, void* dZ, int64_t ldg, int sm_count,
+                           uint32_t* status);
+
+// Exact causal attention (k_attn_exact.cu, k_attn_exact_tc.cu): heads in columns
+// [h head_dim, (h+1) head_dim) of rows with the given strides (elements).
+struct AttnArgs {
+  const void *Q, *K, *V, *O_in, *E;  // O_in, E: backward
+  void *O, *dQ, *dK, *dV;
+  const float* lse;  // T x H, natural log (backward)
+  float* lse_out;    // T x H (forward)
+  float* delta;      // T x H scratch: <o, e> (backward)
+  const int32_t* cu;  // n_seqs + 1 row offsets, or null: sequences of max_len
+  int64_t T;
+  int n_seqs, max_len, H, Hkv, head_dim, dtype;
+  float scale;
+  int64_t ldq, ldk, ldv, ldo, lde, lddq, lddk, lddv;
+  uint32_t* status;
+};
+// Rows [*beg, *end) of a sequence; false where the offsets decrease, leave
+// [0, T] or give more than max_len rows.
+__device__ __forceinline__ bool attn_sequence(const AttnArgs& a, int seq, int64_t* beg,
+                                              int64_t* end) {
+  if (a.cu) {
+    *beg = a.cu[seq];
+    *end = a.cu[seq + 1];
+  } else {
+    *beg = (int64_t)seq * a.max_len;
+    *end = *beg + a.max_len;
+  }
+  return *beg >= 0 && *end >= *beg && *end <= a.T && *end - *beg <= a.max_len;
+}
+cudaError_t launch_attn_exact_simt(cudaStream_t st, const AttnArgs& a, bool backward);
 
 }  // namespace dust

@@ -1,0 +1,773 @@
+// Losses over the vocabulary on logits a model has already produced: log
+// probabilities of given tokens with entropy and top alternatives, and
+// distillation from a teacher's top logits with its logit gradient.
+//
+// Mathematics. Per row, with m = max_j z_j and e_j = exp((z_j - m) / tau):
+//   s = sum_j e_j,  log p_j = (z_j - m) / tau - log s,
+//   entropy (tau = 1) = log s - u / s,  u = sum_j (z_j - m) e_j,
+//   distillation over the teacher's kept set J, q = softmax_J(v / tau):
+//     loss = tau^2 sum_J q_j (log q_j - log p_j),
+//     d loss / d z_j = tau (p_j - q_j)   (q_j = 0 outside J).
+// All sums run in fp32 with the running maximum of an online softmax, so a row
+// is read from HBM once whatever its scale; a thread keeps (m, s, u) of its own
+// elements and the threads' triples are combined in a fixed order, so results
+// do not depend on timing. z - m is formed before the scale is applied:
+// the type's lowest value then stays an ordinary (if unlikely) logit instead of
+// overflowing to -inf, and -inf - m gives exp = 0 without a NaN.
+//
+// Few rows do not fill the GPU with one CTA each, so a row may be split over a
+// cluster of up to 8 CTAs whose triples (and top lists) meet in distributed
+// shared memory: still one launch.
+#include <cfloat>
+
+#include "internal.cuh"
+#include "tc_ptx.cuh"
+
+namespace dust {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kMaxCluster = 8;  // portable cluster size
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float load_f(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float load_f(const __nv_bfloat16* p) {
+  return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p)) << 16);
+}
+// The same for memory that the kernel itself may overwrite later.
+__device__ __forceinline__ float load_rw(const float* p) {
+  return *reinterpret_cast<const volatile float*>(p);
+}
+__device__ __forceinline__ float load_rw(const __nv_bfloat16* p) {
+  return __uint_as_float((uint32_t)*reinterpret_cast<const volatile unsigned short*>(p) << 16);
+}
+__device__ __forceinline__ void store_e(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_e(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// 16 bytes as 4 fp32 or 8 bf16 values.
+template <typename E>
+struct Vec {
+  static constexpr int N = 16 / sizeof(E);
+};
+__device__ __forceinline__ void unpack(const uint4& w, float (&v)[4]) {
+  v[0] = __uint_as_float(w.x);
+  v[1] = __uint_as_float(w.y);
+  v[2] = __uint_as_float(w.z);
+  v[3] = __uint_as_float(w.w);
+}
+__device__ __forceinline__ void unpack(const uint4& w, float (&v)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack(const float (&v)[4]) {
+  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                    __float_as_uint(v[3]));
+}
+__device__ __forceinline__ uint4 pack(const float (&v)[8]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    u[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// A CTA's part of a row: `head` elements up to the first 16-byte boundary (rank
+// 0's), whole vectors [v0, v1) of the aligned body, and the `tail` after it
+// (the last rank's). body = head, in elements from the row's start.
+struct Slice {
+  int64_t head, v0, v1, tail0, tail1;
+};
+template <typename E>
+__device__ __forceinline__ Slice slice_of(const E* row, int64_t V, int rank, int ranks) {
+  constexpr int N = Vec<E>::N;
+  Slice s;
+  int64_t head = (int64_t)(((16 - ((uintptr_t)row & 15)) & 15) / sizeof(E));
+  if (head > V) head = V;
+  const int64_t nv = (V - head) / N;
+  s.head = head;
+  s.v0 = nv * rank / ranks;
+  s.v1 = nv * (rank + 1) / ranks;
+  s.tail0 = head + nv * N;
+  s.tail1 = rank == ranks - 1 ? V : s.tail0;
+  return s;
+}
+
+// Running softmax statistics: maximum, sum of exponentials relative to it and
+// (ENT) the sum of (z - m) exp(z - m). The maximum starts at the type's lowest
+// finite value, so a row of -inf alone leaves s = 0; a NaN (or +inf) element
+// leaves s = NaN.
+struct Stat {
+  float m, s, u;
+};
+__device__ __forceinline__ Stat stat_none() { return Stat{-FLT_MAX, 0.0f, 0.0f}; }
+
+template <bool ENT>
+__device__ __forceinline__ void stat_rescale(Stat& a, float m, float k2) {
+  const float f = ex2((a.m - m) * k2);
+  // f = 0: nothing of the old sums is left (and s (m - m') could be 0 x inf)
+  if (ENT) a.u = f > 0.0f ? f * fmaf(a.s, a.m - m, a.u) : 0.0f;
+  a.s *= f;
+  a.m = m;
+}
+
+template <bool ENT, int N>
+__device__ __forceinline__ void stat_add(Stat& a, const float (&z)[N], float k2) {
+  float cm = z[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) cm = fmaxf(cm, z[i]);
+  if (cm > a.m) stat_rescale<ENT>(a, cm, k2);
+  float s[2] = {0.0f, 0.0f}, u[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float d = z[i] - a.m;
+    const float e = ex2(d * k2);
+    s[i & 1] += e;
+    // exp(-1e4) = 0: the clamp only keeps 0 x (-inf) out
+    if (ENT) u[i & 1] = fmaf(fmaxf(d, -1e4f), e, u[i & 1]);
+  }
+  a.s += s[0] + s[1];
+  if (ENT) a.u += u[0] + u[1];
+}
+
+template <bool ENT>
+__device__ __forceinline__ Stat stat_join(Stat a, const Stat& b, float k2) {
+  const float m = fmaxf(a.m, b.m);
+  Stat c = b;
+  stat_rescale<ENT>(a, m, k2);
+  stat_rescale<ENT>(c, m, k2);
+  a.s += c.s;
+  if (ENT) a.u += c.u;
+  return a;
+}
+
+// The CTA's statistics, the same value in every thread: butterflies inside the
+// warps (every lane combines the same pairs), then the warps in order.
+template <bool ENT>
+__device__ __forceinline__ Stat stat_block(Stat a, float k2, Stat* sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    Stat b = stat_none();
+    b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
+    b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
+    if (ENT) b.u = __shfl_xor_sync(0xffffffffu, a.u, o);
+    a = stat_join<ENT>(a, b, k2);
+  }
+  if (lane == 0) sh[warp] = a;
+  __syncthreads();
+  Stat t = sh[0];
+  for (int w = 1; w < warps; ++w) t = stat_join<ENT>(t, sh[w], k2);
+  return t;
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t addr) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// The row's statistics from its CTAs', the same in every thread of the cluster.
+// `mine` (shared memory) stays readable by the others until the cluster's next
+// barrier, which the caller makes before it leaves.
+template <bool ENT>
+__device__ __forceinline__ Stat stat_cluster(const Stat& a, float k2, Stat* mine, int ranks) {
+  if (ranks == 1) return a;
+  if (threadIdx.x == 0) *mine = a;
+  ptx::cluster_sync();
+  const uint32_t here = ptx::smem_u32(mine);
+  Stat t = stat_none();
+  for (int r = 0; r < ranks; ++r) {
+    const uint32_t p = ptx::mapa_shared(here, (uint32_t)r);
+    Stat b = stat_none();
+    b.m = ld_cluster_f32(p);
+    b.s = ld_cluster_f32(p + 4);
+    if (ENT) b.u = ld_cluster_f32(p + 8);
+    t = r == 0 ? b : stat_join<ENT>(t, b, k2);
+  }
+  return t;
+}
+
+__device__ __forceinline__ float nan_f() { return __int_as_float(0x7fc00000); }
+__device__ __forceinline__ float inf_f() { return __int_as_float(0x7f800000); }
+
+// ---- log probabilities, entropy, top alternatives -----------------------------------
+//
+// Bound by reading the logits once. Without alternatives a thread streams
+// vectors straight into its running statistics. With them, a CTA also keeps the
+// elements that may still be among its n best in a shared-memory list: an element
+// enters when it is not below the CTA's threshold, and when the list has grown
+// past its limit it is sorted, cut to n, and the threshold moves to the n-th.
+// The first threshold is the n-th largest of the threads' maxima over the
+// first tile (n elements at least are not below it), so on ordinary rows about
+// n (1 + ln(V / tile)) elements ever enter. Any row is handled: a tile that
+// enters whole fits the list. List order depends on timing, the sorted list
+// does not: keys are (value, ~index), all different.
+constexpr int kLpThreads = 256;
+constexpr int kTopTile = 8;                           // elements per thread and tile
+constexpr int kTopTileElems = kLpThreads * kTopTile;  // a tile
+constexpr int kTopList = 4096;                        // list entries, a power of two
+constexpr int kTopCut = 512;                          // the list is cut when it grows past this
+static_assert(kTopCut + 16 + kTopTileElems <= kTopList, "a tile must fit the list");
+static_assert(kTopLimit <= kLpThreads && kTopLimit < kTopCut, "one output entry per thread");
+static_assert(kMaxCluster * kTopLimit <= kTopList, "the CTAs' lists meet in one");
+
+__device__ __forceinline__ uint32_t order_bits(float z) {
+  const uint32_t b = __float_as_uint(z + 0.0f);  // -0 counts as +0
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t o) {
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+}
+__device__ __forceinline__ uint64_t top_key(float z, int64_t col) {
+  return ((uint64_t)order_bits(z) << 32) | (uint32_t)(0xffffffffu - (uint32_t)col);
+}
+// The smallest float above z: z' >= next_up(z) exactly when z' > z.
+__device__ __forceinline__ float next_up(float z) {
+  return order_value(order_bits(z) + 1u);
+}
+
+// Sort list[0, count) descending; entries up to the next power of two are
+// cleared to 0 (below every key). All threads of the CTA; ends with a barrier.
+__device__ void sort_list(uint64_t* list, int count) {
+  int P = 32;
+  while (P < count) P <<= 1;
+  for (int i = count + threadIdx.x; i < P; i += blockDim.x) list[i] = 0;
+  __syncthreads();
+  for (int k = 2; k <= P; k <<= 1) {
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      for (int i = threadIdx.x; i < P / 2; i += blockDim.x) {
+        const int a = 2 * i - (i & (j - 1)), b = a + j;
+        const uint64_t x = list[a], y = list[b];
+        if ((x < y) == ((a & k) == 0)) {
+          list[a] = y;
+          list[b] = x;
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+struct TopState {
+  int count;
+  float thr;  // elements >= thr enter
+};
+
+struct LogprobArgs {
+  int64_t ld, V;
+  const int32_t* tokens;  // or null
+  int n;                  // alternatives
+  float* logp;            // or null
+  float* entropy;         // or null
+  int32_t* top_ids;
+  float* top_logp;
+  uint32_t* status;
+};
+
+template <typename E, bool TOP>
+__global__ __launch_bounds__(kLpThreads) void k_token_logprobs(const E* __restrict__ Z,
+                                                               LogprobArgs a, int ranks) {
+  constexpr int N = Vec<E>::N;
+  constexpr int U = TOP ? kTopTile / N : 16 / N;  // vectors per thread and tile
+  extern __shared__ uint64_t list[];              // TOP
+  __shared__ Stat sh_warp[kLpThreads / 32], sh_cta;
+  __shared__ TopState top;
+  const int tid = threadIdx.x;
+  const int rank = ranks > 1 ? (int)ptx::cluster_ctarank() : 0;
+  const int64_t t = blockIdx.x / ranks;
+  const E* row = Z + t * a.ld;
+  const Slice sl = slice_of(row, a.V, rank, ranks);
+  const uint4* body = reinterpret_cast<const uint4*>(row + sl.head);
+  Stat st = stat_none();
+  bool grown = false;
+  if (TOP) {
+    if (tid == 0) {
+      top.count = 0;
+      top.thr = -FLT_MAX;
+    }
+    __syncthreads();
+  }
+  auto enter = [&](float z, int64_t col) {
+    const int slot = atomicAdd(&top.count, 1);
+    list[slot] = top_key(z, col);
+    grown |= slot >= kTopCut;
+  };
+  auto edge = [&](int64_t col) {
+    const float z = load_f(row + col);
+    const float one[1] = {z};
+    stat_add<true, 1>(st, one, kLog2e);
+    if (TOP && z >= top.thr) enter(z, col);
+  };
+  if (rank == 0 && tid < sl.head) edge(tid);
+  // sort, cut to the n best and move the threshold past the n-th: every later
+  // element has a higher index, so among equal values it loses
+  auto cut = [&]() {
+    const int count = top.count;
+    sort_list(list, count);
+    if (tid == 0) {
+      if (count >= a.n) {
+        top.count = a.n;
+        top.thr = next_up(order_value((uint32_t)(list[a.n - 1] >> 32)));
+      }
+    }
+    grown = false;
+    __syncthreads();
+  };
+
+  uint4 w[U];
+  auto fetch = [&](int64_t v) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int64_t k = v + (int64_t)i * kLpThreads + tid;
+      if (k < sl.v1) w[i] = __ldcs(body + k);
+    }
+  };
+  fetch(sl.v0);
+  for (int64_t v = sl.v0; v < sl.v1; v += (int64_t)U * kLpThreads) {
+    float z[U][N];
+    float cm[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int64_t k = v + (int64_t)i * kLpThreads + tid;
+      if (k < sl.v1) {
+        unpack(w[i], z[i]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < N; ++q) z[i][q] = -inf_f();
+      }
+    }
+    fetch(v + (int64_t)U * kLpThreads);  // the next tile's loads run under this tile's math
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      stat_add<true, N>(st, z[i], kLog2e);
+      if (TOP) {
+        cm[i] = z[i][0];
+#pragma unroll
+        for (int q = 1; q < N; ++q) cm[i] = fmaxf(cm[i], z[i][q]);
+      }
+    }
+    if (TOP) {
+      if (v == sl.v0) {
+        // the first threshold: the head elements already listed stay
+        float mx = cm[0];
+#pragma unroll
+        for (int i = 1; i < U; ++i) mx = fmaxf(mx, cm[i]);
+        __syncthreads();
+        uint64_t* scratch = list + 2048;  // apart from the head's entries
+        scratch[tid] = (uint64_t)order_bits(mx) << 32 | (uint32_t)tid;
+        __syncthreads();
+        sort_list(scratch, kLpThreads);
+        if (tid == 0) {
+          const float b = order_value((uint32_t)(scratch[a.n - 1] >> 32));
+          top.thr = fmaxf(b, -FLT_MAX);
+        }
+        __syncthreads();
+      }
+      const float thr = top.thr;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (cm[i] >= thr) {
+          const int64_t col = sl.head + (v + (int64_t)i * kLpThreads + tid) * N;
+#pragma unroll
+          for (int q = 0; q < N; ++q)
+            if (z[i][q] >= thr) enter(z[i][q], col + q);
+        }
+      }
+      if (__syncthreads_or(grown)) cut();
+    }
+  }
+  if (sl.tail0 + tid < sl.tail1) edge(sl.tail0 + tid);
+
+  st = stat_block<true>(st, kLog2e, sh_warp);
+  if (TOP) {  // (the barrier inside stat_block ordered the last entries)
+    const int count = top.count;
+    sort_list(list, count);
+    if (tid == 0) top.count = min(count, a.n);
+    __syncthreads();
+  }
+  const Stat all = stat_cluster<true>(st, kLog2e, &sh_cta, ranks);
+  if (TOP && ranks > 1 && rank == 0) {
+    // the CTAs' sorted lists behind one another, then one sort
+    int total = top.count;
+    for (int r = 1; r < ranks; ++r) {
+      const int cnt = __float_as_int(
+          ld_cluster_f32(ptx::mapa_shared(ptx::smem_u32(&top.count), (uint32_t)r)));
+      const uint32_t src = ptx::mapa_shared(ptx::smem_u32(list), (uint32_t)r);
+      for (int i = tid; i < cnt; i += kLpThreads) list[total + i] = ld_cluster_u64(src + 8u * i);
+      total += cnt;
+    }
+    __syncthreads();
+    sort_list(list, total);
+    if (tid == 0) top.count = min(total, a.n);
+    __syncthreads();
+  }
+  if (rank == 0) {
+    const float logs = logf(all.s);
+    const bool bad = isnan(all.s), empty = all.s == 0.0f;
+    if (tid == 0) {
+      if (a.logp) {
+        const int32_t y = a.tokens[t];
+        float lp;
+        if (y == -1) {
+          lp = 0.0f;
+        } else if (y < 0 || (int64_t)y >= a.V) {
+          atomicOr(a.status, kStatusBadTarget);
+          lp = nan_f();
+        } else {
+          lp = bad ? nan_f() : (empty ? -inf_f() : (load_f(row + y) - all.m) - logs);
+        }
+        a.logp[t] = lp;
+      }
+      if (a.entropy) a.entropy[t] = bad ? nan_f() : (empty ? 0.0f : fmaxf(logs - all.u / all.s, 0.0f));
+    }
+    if (TOP && tid < a.n) {
+      const bool there = tid < top.count && !bad;
+      const uint64_t key = there ? list[tid] : 0;
+      a.top_ids[t * a.n + tid] = there ? (int32_t)(0xffffffffu - (uint32_t)key) : -1;
+      a.top_logp[t * a.n + tid] =
+          bad ? nan_f() : (there ? (order_value((uint32_t)(key >> 32)) - all.m) - logs : -inf_f());
+    }
+  }
+  if (ranks > 1) ptx::cluster_sync();  // the others' shared memory is no longer read
+}
+
+// ---- distillation from a teacher's top logits ---------------------------------------
+//
+// The gradient reads and writes every logit once, which is its bound: 2 V
+// elements a row. A CTA copies its part of the row into shared memory by bulk
+// copies, takes the statistics from the chunks as they land, and forms the
+// gradient from shared memory, so HBM is read once whatever L2 holds. Two CTAs
+// share an SM: one writes while the other's copies are in flight. A row longer
+// than a CTA's buffer is split over a cluster; past 8 buffers (kReread) the
+// second pass reads the row from global memory again.
+enum DistillMode { kLossOnly = 0, kResident = 1, kReread = 2 };
+constexpr int kDsThreads = 512;
+constexpr int kMaxTeacher = kTopLimit;
+constexpr int kChunk = 8192;                // bytes of one bulk copy
+constexpr int kBufBytes = 13 * kChunk;      // 104 KB: two CTAs fit an SM's shared memory
+constexpr int kMaxChunks = kBufBytes / kChunk;
+
+struct DistillArgs {
+  int64_t ld, ldg, V;
+  const int32_t* ids;    // T x k
+  const float* vals;     // T x k
+  int k;
+  float tau, k2;         // temperature, log2(e) / tau
+  const float* weights;  // T or null
+  float* loss;           // T or null
+  uint32_t* status;
+};
+
+struct DistillShared {
+  Stat warp[kDsThreads / 32], cta;
+  float q[kMaxTeacher], z[kMaxTeacher], red[4];
+  int32_t id[kMaxTeacher];
+  uint64_t bar[kMaxChunks];
+};
+
+constexpr uint64_t kCopyWaitNs = 2000000000ull;  // 2 s
+
+// Wait for a chunk's copy, for at most kCopyWaitNs: past that the call reports
+// a timeout and its outputs are unspecified. Every chunk is waited for, so no
+// copy is in flight when the CTA leaves.
+__device__ __noinline__ void wait_copy(uint32_t bar, uint32_t* status) {
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (!ptx::mbar_try_wait(bar, 0)) {
+    if (ptx::globaltimer_ns() - t0 > kCopyWaitNs) {
+      atomicOr(status, kStatusTimeout);
+      return;
+    }
+  }
+}
+
+template <typename E, int MODE>
+__global__ __launch_bounds__(kDsThreads, 2) void k_distill(const E* Z, E* dZ, DistillArgs a,
+                                                        int ranks) {
+  constexpr int N = Vec<E>::N;
+  extern __shared__ __align__(128) uint8_t buf[];  // kResident: the slice's vectors
+  __shared__ DistillShared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = ranks > 1 ? (int)ptx::cluster_ctarank() : 0;
+  const int64_t t = blockIdx.x / ranks;
+  const E* row = Z + t * a.ld;
+  E* out = MODE == kLossOnly ? nullptr : dZ + t * a.ldg;
+  const Slice sl = slice_of(row, a.V, rank, ranks);
+  const uint4* body = reinterpret_cast<const uint4*>(row + sl.head);
+  const float weight = a.weights ? a.weights[t] : 1.0f;
+
+  // the teacher's distribution over its kept set, by the first warps: one
+  // entry per thread, absent where its id is -1 or its value -inf
+  int32_t id = -1;
+  float v = -inf_f();
+  if (tid < a.k) {
+    id = a.ids[t * a.k + tid];
+    if (id != -1) {
+      if (id < 0 || (int64_t)id >= a.V) {
+        atomicOr(a.status, kStatusBadTarget);
+        id = -1;
+      } else {
+        v = a.vals[t * a.k + tid];
+        if (v == -inf_f()) id = -1;
+      }
+    }
+    sh.id[tid] = id;
+  }
+  // a row without a teacher entry, or of weight 0, is left out: its logits are not read
+  const bool live = __syncthreads_or(id >= 0) && weight != 0.0f;
+  // the slice's columns of the gradient, [c0, c1)
+  const int64_t c0 = rank == 0 ? 0 : sl.head + sl.v0 * N;
+  const int64_t c1 = rank == ranks - 1 ? a.V : sl.head + sl.v1 * N;
+  if (!live) {
+    if (MODE != kLossOnly)
+      for (int64_t c = c0 + tid; c < c1; c += kDsThreads) store_e(out + c, 0.0f);
+    if (rank == 0 && tid == 0 && a.loss) a.loss[t] = 0.0f;
+    return;  // every CTA of the cluster leaves here together
+  }
+  const int nbytes = (int)((sl.v1 - sl.v0) * 16);
+  const int chunks = MODE == kResident ? (nbytes + kChunk - 1) / kChunk : 0;
+  if (MODE == kResident && tid == 0) {
+    for (int c = 0; c < chunks; ++c) ptx::mbar_init(ptx::smem_u32(&sh.bar[c]), 1);
+    ptx::fence_barrier_init();
+    ptx::fence_proxy_async();
+    for (int c = 0; c < chunks; ++c) {
+      const uint32_t n = (uint32_t)min(kChunk, nbytes - c * kChunk);
+      const uint32_t bar = ptx::smem_u32(&sh.bar[c]);
+      ptx::mbar_expect_tx(bar, n);
+      ptx::bulk_load(ptx::smem_u32(buf) + c * kChunk,
+                     reinterpret_cast<const uint8_t*>(body + sl.v0) + c * kChunk, n, bar);
+    }
+  }
+  // the student's logits at the teacher's entries, before any are overwritten
+  // (dZ may be Z), and q
+  float zj = 0.0f;
+  if (id >= 0) zj = load_rw(row + id);
+  if (tid < a.k) sh.z[tid] = zj;
+  if (warp < kMaxTeacher / 32) {
+    float mx = v;  // NaN and +inf values make the row's loss NaN below
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (lane == 0) sh.red[warp] = mx;
+  }
+  __syncthreads();
+  const float vm = fmaxf(fmaxf(sh.red[0], sh.red[1]), fmaxf(sh.red[2], sh.red[3]));
+  float eq = 0.0f;
+  if (id >= 0) eq = expf((v - vm) / a.tau);
+  __syncthreads();
+  if (warp < kMaxTeacher / 32) {
+    float sq = eq;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    if (lane == 0) sh.red[warp] = sq;
+  }
+  __syncthreads();
+  const float qsum = (sh.red[0] + sh.red[1]) + (sh.red[2] + sh.red[3]);
+  const float q = eq / qsum;
+  if (tid < a.k) sh.q[tid] = id >= 0 ? q : 0.0f;
+
+  // statistics of the row
+  Stat st = stat_none();
+  auto edge = [&](int64_t col) {
+    const float one[1] = {load_rw(row + col)};
+    stat_add<false, 1>(st, one, a.k2);
+  };
+  if (rank == 0 && tid < sl.head) edge(tid);
+  if (sl.tail0 + tid < sl.tail1) edge(sl.tail0 + tid);
+  if (MODE == kResident) {
+    for (int c = 0; c < chunks; ++c) {
+      if (!ptx::mbar_try_wait(ptx::smem_u32(&sh.bar[c]), 0))
+        wait_copy(ptx::smem_u32(&sh.bar[c]), a.status);
+      const int n = min(kChunk, nbytes - c * kChunk) / 16;
+      const uint4* src = reinterpret_cast<const uint4*>(buf + c * kChunk);
+      for (int i = tid; i < n; i += kDsThreads) {
+        float z[N];
+        unpack(src[i], z);
+        stat_add<false, N>(st, z, a.k2);
+      }
+    }
+  } else {
+    constexpr int U = 16 / N;
+    uint4 w[U];
+    auto fetch = [&](int64_t p) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int64_t k = p + (int64_t)i * kDsThreads + tid;
+        if (k < sl.v1) w[i] = MODE == kReread ? body[k] : __ldcs(body + k);
+      }
+    };
+    fetch(sl.v0);
+    for (int64_t p = sl.v0; p < sl.v1; p += (int64_t)U * kDsThreads) {
+      float z[U][N];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (p + (int64_t)i * kDsThreads + tid < sl.v1) {
+          unpack(w[i], z[i]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < N; ++j) z[i][j] = -inf_f();
+        }
+      }
+      fetch(p + (int64_t)U * kDsThreads);
+#pragma unroll
+      for (int i = 0; i < U; ++i) stat_add<false, N>(st, z[i], a.k2);
+    }
+  }
+  st = stat_block<false>(st, a.k2, sh.warp);
+  // (for dZ = Z, the cluster's barrier in here also orders the gathers above
+  // before the first store)
+  const Stat all = stat_cluster<false>(st, a.k2, &sh.cta, ranks);
+  const float logs = logf(all.s);  // -inf for a row of -inf: log p = -inf, loss = +inf
+
+  if (rank == 0 && a.loss && warp == 0) {
+    // entries in order, four strides of 32, then a fixed butterfly
+    float acc = 0.0f;
+    for (int j = lane; j < a.k; j += 32) {
+      const float qj = sh.q[j];
+      if (qj != 0.0f) {
+        const float lq = (a.vals[t * a.k + j] - vm) / a.tau - logf(qsum);
+        const float lp = all.s == 0.0f ? -inf_f() : (sh.z[j] - all.m) / a.tau - logs;
+        acc = fmaf(qj, lq - lp, acc);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if (lane == 0) a.loss[t] = a.tau * a.tau * acc;
+  }
+  if (MODE != kLossOnly) {
+    const float scale = weight * a.tau;
+    const float r = all.s == 0.0f ? 0.0f : scale / all.s;  // NaN rows stay NaN
+    auto grad = [&](float z) { return r * ex2((z - all.m) * a.k2); };
+    auto at = [&](int64_t col) -> float {
+      const int64_t e = col - sl.head - sl.v0 * N;  // element of the slice's body
+      if (MODE == kResident && e >= 0 && e < (sl.v1 - sl.v0) * N) {
+        return load_rw(reinterpret_cast<const E*>(buf) + e);
+      }
+      return load_rw(row + col);
+    };
+    if ((((uintptr_t)out ^ (uintptr_t)row) & 15) == 0) {
+      // the gradient's rows are aligned as the logits' are: whole vectors
+      uint4* dst = reinterpret_cast<uint4*>(out + sl.head) + sl.v0;
+      const uint4* src = MODE == kResident ? reinterpret_cast<const uint4*>(buf) : body + sl.v0;
+      const int64_t n = sl.v1 - sl.v0;
+      for (int64_t i = tid; i < n; i += kDsThreads) {
+        float z[N];
+        unpack(src[i], z);
+#pragma unroll
+        for (int j = 0; j < N; ++j) z[j] = grad(z[j]);
+        __stcs(dst + i, pack(z));
+      }
+      if (rank == 0 && tid < sl.head) store_e(out + tid, grad(at(tid)));
+      if (sl.tail0 + tid < sl.tail1) store_e(out + sl.tail0 + tid, grad(at(sl.tail0 + tid)));
+    } else {
+      for (int64_t c = c0 + tid; c < c1; c += kDsThreads) store_e(out + c, grad(at(c)));
+    }
+    // the teacher's entries of this CTA's columns: p - q in fp32, rounded once;
+    // an id that the teacher lists twice has both weights, in list order
+    __syncthreads();
+    if (id >= 0 && id >= c0 && id < c1) {
+      float qs = 0.0f;
+      for (int j = 0; j < a.k; ++j)
+        if (sh.id[j] == id) qs += sh.q[j];
+      store_e(out + id, grad(zj) - scale * qs);
+    }
+  }
+  if (ranks > 1) ptx::cluster_sync();  // the others' shared memory is no longer read
+}
+
+// CTAs per row: at least `need`; more while the rows leave SMs without a CTA and
+// every CTA keeps a tile of its own to read.
+int cluster_for(int64_t T, int64_t V, int need, int64_t tile, int sm_count) {
+  int c = need;
+  while (2 * c <= kMaxCluster && T * 2 * c <= sm_count && V >= 2 * c * tile) c *= 2;
+  return c;
+}
+
+template <typename F, typename... Args>
+cudaError_t launch_rows(cudaStream_t st, F fn, int64_t T, int ranks, int threads, size_t smem,
+                        Args... args) {
+  cudaError_t err = cudaSuccess;
+  if (smem > 48 * 1024)
+    err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ranks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(T * ranks));
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  err = cudaLaunchKernelEx(&cfg, fn, args..., ranks);
+  return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+template <typename E>
+cudaError_t logprobs_as(cudaStream_t st, const void* Z, int64_t T, const LogprobArgs& a,
+                        int sm_count) {
+  const E* z = (const E*)Z;
+  const int c = cluster_for(T, a.V, 1, kTopTileElems, sm_count);
+  if (a.n > 0)
+    return launch_rows(st, k_token_logprobs<E, true>, T, c, kLpThreads,
+                       (size_t)kTopList * sizeof(uint64_t), z, a);
+  return launch_rows(st, k_token_logprobs<E, false>, T, c, kLpThreads, 0, z, a);
+}
+
+template <typename E>
+cudaError_t distill_as(cudaStream_t st, const void* Z, void* dZ, int64_t T, const DistillArgs& a,
+                       int sm_count) {
+  const E* z = (const E*)Z;
+  E* g = (E*)dZ;
+  const int64_t tile = (int64_t)kDsThreads * 16;
+  if (!g)
+    return launch_rows(st, k_distill<E, kLossOnly>, T, cluster_for(T, a.V, 1, tile, sm_count),
+                       kDsThreads, 0, z, g, a);
+  const int64_t need = (a.V * (int64_t)sizeof(E) + kBufBytes - 1) / kBufBytes;
+  if (need > kMaxCluster)
+    return launch_rows(st, k_distill<E, kReread>, T, kMaxCluster, kDsThreads, 0, z, g, a);
+  return launch_rows(st, k_distill<E, kResident>, T,
+                     cluster_for(T, a.V, (int)need, tile, sm_count), kDsThreads,
+                     (size_t)kBufBytes, z, g, a);
+}
+
+}  // namespace
+
+cudaError_t launch_token_logprobs(cudaStream_t st, const void* Z, int dtype, int64_t T, int64_t V,
+                                  int64_t ld, const int32_t* tokens, int top, float* logp,
+                                  float* entropy, int32_t* top_ids, float* top_logp, int sm_count,
+                                  uint32_t* status) {
+  if (T <= 0) return cudaSuccess;
+  const LogprobArgs a{ld, V, tokens, top, logp, entropy, top_ids, top_logp, status};
+  return dtype == DUST_BF16 ? logprobs_as<__nv_bfloat16>(st, Z, T, a, sm_count)
+                            : logprobs_as<float>(st, Z, T, a, sm_count);
+}
+
+cudaError_t launch_distill(cudaStream_t st, const void* Z, int dtype, int64_t T, int64_t V,
+                           int64_t ld, const int32_t* ids, const float* vals, int k, float tau,
+                           const float* weights, float* loss, void* dZ, int64_t ldg, int sm_count,
+                           uint32_t* status) {
+  if (T <= 0) return cudaSuccess;
+  const DistillArgs a{ld, ldg, V, ids, vals, k, tau, kLog2e / tau, weights, loss, status};
+  return dtype == DUST_BF16 ? distill_as<__nv_bfloat16>(st, Z, dZ, T, a, sm_count)
+                            : distill_as<float>(st, Z, dZ, T, a, sm_count);
+}
+
+}  // namespace dust
