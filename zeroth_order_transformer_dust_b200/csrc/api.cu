@@ -324,11 +324,11 @@ dust_status check_attn_dims(dust_ctx* ctx, const dust_attn_dims* d, AttnArgs* a)
   if (d->n_kv_heads < 1 || d->n_heads < 1 || d->n_heads > 65535 || d->n_heads % d->n_kv_heads)
     return fail(ctx, DUST_ERR_ARG,
                 "n_heads must lie in [1, 65535] and be a multiple of n_kv_heads >= 1");
-  if (d->n_seqs < 0 || d->n_seqs > 65535)
-    return fail(ctx, DUST_ERR_ARG, "n_seqs must lie in [0, 65535]");
+  if (d->n_seqs < 0 || d->n_seqs > 65535 || (int64_t)d->n_seqs * d->n_heads > 0x7fffffffLL)
+    return fail(ctx, DUST_ERR_ARG, "n_seqs must lie in [0, 65535], n_seqs n_heads below 2^31");
   if (d->T < 0 || d->T > 0x7fffffffLL) return fail(ctx, DUST_ERR_ARG, "T must lie in [0, 2^31)");
-  if (d->max_len < 1 || d->max_len > (1 << 24))
-    return fail(ctx, DUST_ERR_ARG, "max_len must lie in [1, 2^24]");
+  if (d->max_len < 1 || d->max_len > (1 << 22))
+    return fail(ctx, DUST_ERR_ARG, "max_len must lie in [1, 2^22]");
   if (!d->cu_seqlens && (int64_t)d->n_seqs * d->max_len > d->T)
     return fail(ctx, DUST_ERR_ARG, "n_seqs sequences of max_len rows exceed T");
   if (!std::isfinite(d->scale) || d->scale < 0.0f)
@@ -1143,7 +1143,9 @@ dust_status dust_attn_forward(dust_ctx* ctx, const dust_attn_dims* dims, const v
   a.Q = Q; a.K = Kc; a.V = Vc; a.O = O_out; a.lse_out = lse_out;
   a.status = ctx->d_status;
   mark(ctx, nullptr);
-  DUST_CU(launch_attn_exact_simt(ctx->stream, a, false));
+  DUST_CU(ctx->tc_enabled && attn_exact_tc_supported(a, false)
+              ? launch_attn_exact_tc(ctx->stream, a, false)
+              : launch_attn_exact_simt(ctx->stream, a, false));
   ctx->launches += 1;
   mark(ctx, "attn_forward");
   return finish(ctx, dims->flags);
@@ -1174,7 +1176,9 @@ dust_status dust_attn_backward(dust_ctx* ctx, const dust_attn_dims* dims, const 
   a.dQ = dQ_out; a.dK = dK_out; a.dV = dV_out; a.delta = delta;
   a.status = ctx->d_status;
   mark(ctx, nullptr);
-  DUST_CU(launch_attn_exact_simt(ctx->stream, a, true));
+  DUST_CU(ctx->tc_enabled && attn_exact_tc_supported(a, true)
+              ? launch_attn_exact_tc(ctx->stream, a, true)
+              : launch_attn_exact_simt(ctx->stream, a, true));
   ctx->launches += 2;
   mark(ctx, "attn_backward");
   return finish(ctx, dims->flags);

@@ -466,5 +466,8 @@ __device__ __forceinline__ bool attn_sequence(const AttnArgs& a, int seq, int64_
   return *beg >= 0 && *end >= *beg && *end <= a.T && *end - *beg <= a.max_len;
 }
 cudaError_t launch_attn_exact_simt(cudaStream_t st, const AttnArgs& a, bool backward);
+// Tensor cores: bf16 rows on 16-byte boundaries, head_dim 64 or 128.
+bool attn_exact_tc_supported(const AttnArgs& a, bool backward);
+cudaError_t launch_attn_exact_tc(cudaStream_t st, const AttnArgs& a, bool backward);
 
 }  // namespace dust
