@@ -3,11 +3,11 @@
 //
 // Backward. One kernel body serves both sides. A CTA keeps 128 rows of its side
 // resident (queries with their error signal, or keys with their values) and
-// streams tiles of 64 rows of the other side. Per tile, with the resident rows
+// streams tiles of 128 rows of the other side. Per tile, with the resident rows
 // as TMEM lanes:
-//   query side   S = Q K^T, dP = E V^T (64 columns: keys),
+//   query side   S = Q K^T, dP = E V^T (columns: keys),
 //                dS = P (dP - delta) -> bf16 in TMEM, dQ += dS K;
-//   key side     S^T = K Q^T, dP^T = V E^T (64 columns: queries),
+//   key side     S^T = K Q^T, dP^T = V E^T (columns: queries),
 //                P^T, dS^T -> bf16 in TMEM, dV += P^T E, dK += dS^T Q.
 // The streamed tile is staged once by TMA and read twice: K-major by the score
 // products and MN-major by the gradient products. P and dS never leave the SM:
@@ -16,12 +16,19 @@
 // the CTA's whole life. Rounding P and dS to bf16 (half a step, 2^-8 relative,
 // per term, against fp32 sums) is what puts their products on the tensor cores.
 //
+// Tiles of 128 and not 64 streamed rows: a 128 x 64 x 16 MMA takes as long as a
+// 128 x 128 x 16 one (64 cycles: its A operand is read at the same rate).
+//
 // Warp roles: warp 0 TMA producer, warp 1 MMA issuer, warps 2..9 softmax (two
-// warps per TMEM lane quarter, 32 of the tile's 64 columns each). With 64-wide
-// heads a CTA needs 256 TMEM columns and two CTAs share an SM: one's softmax
-// runs under the other's MMAs. With 128-wide heads the accumulators take half of
-// TMEM, so one CTA has the SM and keeps two score buffers: the next tile's
-// scores are computed while this tile's softmax runs.
+// warps per TMEM lane quarter, 64 of the tile's 128 columns each). The softmax of
+// a tile has two halves, P from S and dS from dP, and the MMAs are ordered so
+// that the tensor pipe works through both: S of the next tile runs while dS is
+// formed, the gradient products and the next dP while the next P is. Where TMEM
+// has room S has two buffers (all but the key side of 128-wide heads).
+//
+// delta = <o, e> is taken from the bf16 output o, whose rounding matters where
+// few keys average it out; in a sequence's first 128 rows the kernel sums
+// P dP instead, which is the same number without that rounding.
 //
 // Rows at or past the end of a sequence belong to nobody or to another
 // sequence, so their content must not enter a sum, not even times 0: in the
@@ -39,39 +46,44 @@ namespace dust {
 namespace {
 
 constexpr int BM = 128;  // resident rows: TMEM lanes
-constexpr int BN = 64;   // rows of a streamed tile
-constexpr int BOX_BYTES = 64 * 64 * 2;  // a TMA box: 64 rows x 64 columns
+constexpr int BN = 128;  // rows of a streamed tile
+constexpr int BOX_BYTES = 128 * 64 * 2;  // a TMA box: 128 rows x 64 columns
 constexpr int SOFT_WARPS = 8;
 constexpr int THREADS = 64 + 32 * SOFT_WARPS;
-constexpr int STAGES = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
-template <int D>
+template <int D, bool KEY>
 struct Cfg {
-  static constexpr int NBUF = D == 128 ? 2 : 1;       // score buffers
-  static constexpr int BOXES = D / 64;                // boxes per 64 rows of a tensor
-  static constexpr int RES_BYTES = 2 * BM * D * 2;    // both resident tensors
-  static constexpr int HALF_STAGE = BN * D * 2;       // one tensor's streamed tile
-  static constexpr int STAGE_BYTES = 2 * HALF_STAGE;
-  static constexpr int ACC_COL = NBUF * 2 * BN;       // TMEM: score buffers, then the sums
-  static constexpr int TMEM_COLS = D == 128 ? 512 : 256;
-  static constexpr size_t SMEM = 1024 + (size_t)RES_BYTES + (size_t)STAGES * STAGE_BYTES + 2048 + 256;
-  static_assert(ACC_COL + 2 * D <= TMEM_COLS, "TMEM columns");
-  static_assert(SMEM * (D == 64 ? 2 : 1) <= 226 * 1024, "shared memory per SM");
+  static constexpr int NS = KEY && D == 128 ? 1 : 2;  // score buffers
+  static constexpr int STAGES = D == 128 ? 2 : 4;
+  static constexpr int BOXES = D / 64;                // boxes per 128 rows of a tensor
+  static constexpr int TILE_BYTES = BM * D * 2;       // 128 rows of a tensor
+  // shared memory: the resident tensors, then the stages of either streamed tensor
+  static constexpr int S0 = 2 * TILE_BYTES, S1 = S0 + STAGES * TILE_BYTES;
+  static constexpr int COL = S1 + STAGES * TILE_BYTES;  // -lse and -delta per stage
+  static constexpr int COL_BYTES = STAGES * 2 * BN * 4;
+  static constexpr size_t SMEM = 1024 + (size_t)COL + COL_BYTES + 256;
+  // TMEM columns: score buffers, dP, the sums
+  static constexpr int DP = NS * BN, ACC = DP + BN;
+  static_assert(ACC + (KEY ? 2 : 1) * D <= 512, "TMEM columns");
+  static_assert(SMEM <= 227 * 1024 && COL_BYTES >= 2 * BM * 4, "shared memory");
 };
 
 struct Bars {
-  uint64_t res, land, full[STAGES], empty[STAGES], sfull[2], pfull[2], vdone[2], afull;
+  uint64_t res, land, full0[4], full1[4], empty0[4], empty1[4], sfull[2], pfull[2], dpfull, dsfull,
+      afull;
   uint32_t tmem_base;
   int abort;
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
 
-// As the GEMM's bounded wait: false (and the abort flag and timeout bit) on expiry.
-__device__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort,
-                             uint32_t* status) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
+// Wait for phase `parity` of an mbarrier, for at most kWaitLimitNs. On expiry the
+// CTA's abort flag and the timeout bit are set and false returns; a raised
+// abort flag also ends the wait. The hand-overs between the warps are short, so
+// the clock is first read after some polls.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort,
+                                       uint32_t* status) {
   const uint64_t t0 = ptx::globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
     if (ptx::mbar_try_wait(bar, parity)) return true;
@@ -84,6 +96,13 @@ __device__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort,
       }
     }
   }
+}
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort,
+                                             uint32_t* status) {
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+  return wait_long(bar, parity, abort, status);
 }
 // The same by a whole warp, with one answer for all lanes.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort,
@@ -127,20 +146,19 @@ __device__ __forceinline__ void store_row(uint32_t taddr, float scale, __nv_bflo
 // S = r0 s0^T and dP = r1 s1^T: (Q, E; K, V) on the query side, (K, V; Q, E) on
 // the key side.
 template <int D, bool KEY>
-__global__ __launch_bounds__(THREADS, D == 64 ? 2 : 1) void k_attn_exact_bwd_tc(
+__global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
     const __grid_constant__ CUtensorMap tmR0, const __grid_constant__ CUtensorMap tmR1,
     const __grid_constant__ CUtensorMap tmS0, const __grid_constant__ CUtensorMap tmS1,
     AttnArgs a) {
-  using C = Cfg<D>;
-  constexpr int NBUF = C::NBUF;
+  using C = Cfg<D, KEY>;
+  constexpr int NS = C::NS, ST = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* basep = smem_raw + (base - raw);
-  const uint32_t sRes = base, sStage = base + C::RES_BYTES;
-  // query side: partial deltas (2 x 128); key side: per stage lse and delta (2 x 64)
-  float* s_col = reinterpret_cast<float*>(basep + C::RES_BYTES + STAGES * C::STAGE_BYTES);
-  Bars* sh = reinterpret_cast<Bars*>(reinterpret_cast<uint8_t*>(s_col) + 2048);
+  // key side: per stage -lse and -delta (2 x 128); query side: partial deltas (2 x 128)
+  float* s_col = reinterpret_cast<float*>(basep + C::COL);
+  Bars* sh = reinterpret_cast<Bars*>(basep + C::COL + C::COL_BYTES);
   volatile int* abort = &sh->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -157,36 +175,41 @@ __global__ __launch_bounds__(THREADS, D == 64 ? 2 : 1) void k_attn_exact_bwd_tc(
   const int len = (int)(end - beg);
   const int r_first = tile * BM;  // first resident row of the sequence
   if (r_first >= len) return;
-  const int tiles64 = (len + BN - 1) / BN;
   // streamed tiles: keys [0, diagonal] of one head, or for every head of the
   // group the queries from the diagonal on
-  const int per_head = KEY ? tiles64 - 2 * tile : min(tiles64, 2 * tile + 2);
+  const int per_head = KEY ? (len + BN - 1) / BN - tile : tile + 1;
   const int n = KEY ? group * per_head : per_head;
-  const int s_off = KEY ? 2 * tile : 0;
+  const int s_off = KEY ? tile : 0;
 
   if (threadIdx.x == 0) {
     ptx::mbar_init(ptx::smem_u32(&sh->res), 1);
     ptx::mbar_init(ptx::smem_u32(&sh->land), 1);
-    for (int s = 0; s < STAGES; ++s) {
-      ptx::mbar_init(ptx::smem_u32(&sh->full[s]), 2);  // the bytes, and the producer's word
-      ptx::mbar_init(ptx::smem_u32(&sh->empty[s]), 1);
+    for (int s = 0; s < ST; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&sh->full0[s]), 2);  // the bytes, and the producer's word
+      ptx::mbar_init(ptx::smem_u32(&sh->full1[s]), 2);
+      ptx::mbar_init(ptx::smem_u32(&sh->empty0[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&sh->empty1[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(ptx::smem_u32(&sh->sfull[b]), 1);
       ptx::mbar_init(ptx::smem_u32(&sh->pfull[b]), SOFT_WARPS);
-      ptx::mbar_init(ptx::smem_u32(&sh->vdone[b]), 1);
     }
+    ptx::mbar_init(ptx::smem_u32(&sh->dpfull), 1);
+    ptx::mbar_init(ptx::smem_u32(&sh->dsfull), SOFT_WARPS);
     ptx::mbar_init(ptx::smem_u32(&sh->afull), 1);
     sh->abort = 0;
     ptx::fence_barrier_init();
     ptx::fence_proxy_async();
-    ptx::prefetch_map(&tmR0);
-    ptx::prefetch_map(&tmR1);
-    ptx::prefetch_map(&tmS0);
-    ptx::prefetch_map(&tmS1);
+    // the resident rows are on their way while TMEM is allocated
+    const uint32_t bar = ptx::smem_u32(&sh->res);
+    ptx::mbar_expect_tx(bar, 2 * C::TILE_BYTES);
+    for (int t = 0; t < 2; ++t)
+      for (int c = 0; c < C::BOXES; ++c)
+        ptx::tma_load_2d(base + t * C::TILE_BYTES + c * BOX_BYTES, t ? &tmR1 : &tmR0,
+                         head * D + 64 * c, (int)(beg + r_first), bar);
   }
   if (warp == 1) {
-    ptx::tmem_alloc(ptx::smem_u32(&sh->tmem_base), C::TMEM_COLS);
+    ptx::tmem_alloc(ptx::smem_u32(&sh->tmem_base), 512);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
@@ -196,171 +219,166 @@ __global__ __launch_bounds__(THREADS, D == 64 ? 2 : 1) void k_attn_exact_bwd_tc(
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
-    const int res_col = head * D;
-    if (lane == 0) {
-      const uint32_t bar = ptx::smem_u32(&sh->res);
-      ptx::mbar_expect_tx(bar, C::RES_BYTES);
-      for (int t = 0; t < 2; ++t)
-        for (int c = 0; c < C::BOXES; ++c)
-          for (int h = 0; h < 2; ++h)
-            ptx::tma_load_2d(sRes + t * (BM * D * 2) + (2 * c + h) * BOX_BYTES, t ? &tmR1 : &tmR0,
-                             res_col + 64 * c, (int)(beg + r_first + 64 * h), bar);
-    }
-    // key side: lse (log2) and delta of a tile's queries, two rows per lane;
-    // +inf past the sequence's end, which makes p = 0 there
-    float nl[2], nd[2];
+    // key side: -lse (log2) and -delta of a tile's queries, four rows per lane;
+    // -inf past the sequence's end, which makes p = 0 there
+    float nl[4], nd[4];
     auto fetch_cols = [&](int j) {
       const int h = head * group + j / per_head;
       const int r = (s_off + j % per_head) * BN;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 4; ++i) {
         const int q = r + lane + 32 * i;
         const bool in = j < n && q < len;
-        nl[i] = in ? a.lse[(beg + q) * a.H + h] * kLog2e : inf_f();
-        nd[i] = in ? a.delta[(beg + q) * a.H + h] : 0.0f;
+        nl[i] = in ? -a.lse[(beg + q) * a.H + h] * kLog2e : -inf_f();
+        nd[i] = in ? -a.delta[(beg + q) * a.H + h] : 0.0f;
       }
     };
     if (KEY) fetch_cols(0);
     uint32_t land_phase = 0;
-    int armed = 0;  // tiles whose copies were issued
-    for (int j = 0; j < n; ++j) {
-      const int st = j % STAGES;
-      const uint32_t ph = (uint32_t)(j / STAGES) & 1u;
-      if (!wait_warp(ptx::smem_u32(&sh->empty[st]), ph ^ 1u, abort, a.status)) break;
+    int armed0 = 0, armed1 = 0;  // tiles of s0 and s1 whose copies were issued
+    // one tile of one streamed tensor into its stage; false after an abort
+    auto load = [&](const CUtensorMap* map, uint32_t off, uint64_t* full, uint64_t* empty, int j,
+                    int* armed) {
+      const int st = j % ST;
+      if (!wait_warp(ptx::smem_u32(&empty[st]), ((uint32_t)(j / ST) & 1u) ^ 1u, abort, a.status))
+        return false;
       const int h = KEY ? head * group + j / per_head : head / group;
       const int r = (s_off + j % per_head) * BN;
-      const uint32_t dst = sStage + (uint32_t)(st * C::STAGE_BYTES);
-      const uint32_t full = ptx::smem_u32(&sh->full[st]), land = ptx::smem_u32(&sh->land);
+      const uint32_t fb = ptx::smem_u32(&full[st]), land = ptx::smem_u32(&sh->land);
       const bool partial = r + BN > len;
       if (lane == 0) {
-        const uint32_t bar = partial ? land : full;
-        ptx::mbar_expect_tx(bar, C::STAGE_BYTES);
-        for (int t = 0; t < 2; ++t)
-          for (int c = 0; c < C::BOXES; ++c)
-            ptx::tma_load_2d(dst + t * C::HALF_STAGE + c * BOX_BYTES, t ? &tmS1 : &tmS0,
-                             h * D + 64 * c, (int)(beg + r), bar);
+        const uint32_t bar = partial ? land : fb;
+        ptx::mbar_expect_tx(bar, C::TILE_BYTES);
+        for (int c = 0; c < C::BOXES; ++c)
+          ptx::tma_load_2d(base + off + st * C::TILE_BYTES + c * BOX_BYTES, map, h * D + 64 * c,
+                           (int)(beg + r), bar);
       }
-      armed = j + 1;
-      if (KEY) {
+      *armed = j + 1;
+      if (KEY && off == C::S0) {
         float* col = s_col + st * 2 * BN;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
           col[lane + 32 * i] = nl[i];
           col[BN + lane + 32 * i] = nd[i];
         }
         fetch_cols(j + 1);
       }
       if (partial) {
-        if (!wait_warp(land, land_phase, abort, a.status)) break;
+        if (!wait_warp(land, land_phase, abort, a.status)) return false;
         land_phase ^= 1u;
         // zero the 128-byte lines of the rows past the end (a swizzled row stays
         // inside its line)
         const int rows = r + BN - len;
-        uint4* st0 = reinterpret_cast<uint4*>(basep + C::RES_BYTES + st * C::STAGE_BYTES);
-        for (int i = lane; i < 2 * C::BOXES * rows * 8; i += 32) {
+        uint4* t = reinterpret_cast<uint4*>(basep + off + st * C::TILE_BYTES);
+        for (int i = lane; i < C::BOXES * rows * 8; i += 32) {
           const int box = i / (rows * 8), w = i % (rows * 8);
-          st0[box * (BOX_BYTES / 16) + (BN - rows) * 8 + w] = make_uint4(0, 0, 0, 0);
+          t[box * (BOX_BYTES / 16) + (BN - rows) * 8 + w] = make_uint4(0, 0, 0, 0);
         }
         ptx::fence_proxy_async();
       }
       __syncwarp();
       if (lane == 0) {
-        if (partial) ptx::mbar_arrive(full);
-        ptx::mbar_arrive(full);
+        if (partial) ptx::mbar_arrive(fb);
+        ptx::mbar_arrive(fb);
       }
-    }
+      return true;
+    };
+    for (int j = 0; j < n; ++j)
+      if (!load(&tmS0, C::S0, sh->full0, sh->empty0, j, &armed0) ||
+          !load(&tmS1, C::S1, sh->full1, sh->empty1, j, &armed1))
+        break;
     // every copy has landed before the CTA can exit (after an abort the last
     // stages may not have been waited for by the MMAs)
     if (*abort) {
       int dummy = 0;
       wait_warp(ptx::smem_u32(&sh->res), 0, &dummy, a.status);
-      for (int j = max(0, armed - STAGES); j < armed; ++j) {
-        const int r = (s_off + j % per_head) * BN;
-        const bool partial = r + BN > len;
-        if (partial)
-          wait_warp(ptx::smem_u32(&sh->land), land_phase, &dummy, a.status);
-        else
-          wait_warp(ptx::smem_u32(&sh->full[j % STAGES]), (uint32_t)(j / STAGES) & 1u, &dummy,
-                    a.status);
-      }
+      auto landed = [&](uint64_t* full, int armed) {
+        for (int j = max(0, armed - ST); j < armed; ++j) {
+          if ((s_off + j % per_head) * BN + BN > len)
+            wait_warp(ptx::smem_u32(&sh->land), land_phase, &dummy, a.status);
+          else
+            wait_warp(ptx::smem_u32(&full[j % ST]), (uint32_t)(j / ST) & 1u, &dummy, a.status);
+        }
+      };
+      landed(sh->full0, armed0);
+      landed(sh->full1, armed1);
     }
   } else if (warp == 1) {
-    // ---------------- MMA issuer ----------------
-    if (lane == 0) {
-      constexpr uint32_t id_s = ptx::idesc_bf16_f32(BM, BN);
-      constexpr uint32_t id_g = ptx::idesc_bf16_f32(BM, D) | ptx::kIdescBMn;
-      // S or dP: K-major operands, 64-column boxes, 32 bytes per 16-deep step
-      auto product = [&](uint32_t d, uint32_t r, uint32_t s) {
+    // ---------------- MMA issuer (the warp together, lane 0 issues) ----------------
+    constexpr uint32_t id_s = ptx::idesc_bf16_f32(BM, BN);
+    constexpr uint32_t id_g = ptx::idesc_bf16_f32(BM, D) | ptx::kIdescBMn;
+    const uint32_t on = lane == 0;
+    // S or dP: K-major operands, 64-column boxes, 32 bytes per 16-deep step
+    auto product = [&](uint32_t d, uint32_t r, uint32_t s) {
+      ptx::tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < C::BOXES; ++c)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            ptx::mma_f16(d, ptx::sdesc_kmajor_sw128(r + c * 2 * BOX_BYTES + 32 * k),
-                         ptx::sdesc_kmajor_sw128(s + c * BOX_BYTES + 32 * k), id_s, (c | k) != 0);
-      };
-      // sum += (bf16 tile in TMEM) x (streamed tile read MN-major: 16 rows, 2048
-      // bytes, per step). The softmax warps of column half h left their 32
-      // columns at 32 h: two steps each.
-      auto gradient = [&](uint32_t acc, uint32_t p, uint32_t s, bool first) {
+      for (int c = 0; c < C::BOXES; ++c)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          ptx::mma_f16_ts(acc, p + 32 * (k >> 1) + 8 * (k & 1),
-                          ptx::sdesc_mnmajor_sw128(s + 2048 * k, BOX_BYTES), id_g,
-                          !first || k != 0);
-      };
-      auto wait = [&](uint64_t& bar, int use) {
-        return wait_bounded(ptx::smem_u32(&bar), (uint32_t)use & 1u, abort, a.status);
-      };
-      const uint32_t acc0 = tmem + C::ACC_COL, acc1 = acc0 + D;
-      bool issued = false;
-      // The score buffer's columns are free once the gradient MMAs that read
-      // them are complete; the second product waits while the first runs.
-      auto scores = [&](int j) {
-        const int st = j % STAGES, b = j % NBUF, o = j - NBUF;
-        const uint32_t s = sStage + (uint32_t)(st * C::STAGE_BYTES);
-        if (!wait(sh->full[st], j / STAGES)) return false;
-        if (KEY && o >= 0 && !wait(sh->vdone[b], o / NBUF)) return false;
-        ptx::tc_fence_after();
-        product(tmem + b * 2 * BN, sRes, s);
-        issued = true;
-        if (o >= 0 && !wait(sh->empty[o % STAGES], o / STAGES)) return false;
-        ptx::tc_fence_after();
-        product(tmem + b * 2 * BN + BN, sRes + BM * D * 2, s + C::HALF_STAGE);
-        ptx::mma_commit(ptx::smem_u32(&sh->sfull[b]));
-        return true;
-      };
-      auto grads = [&](int j) {
-        const int st = j % STAGES, b = j % NBUF;
-        const uint32_t s = sStage + (uint32_t)(st * C::STAGE_BYTES);
-        if (!wait(sh->pfull[b], j / NBUF)) return false;
-        ptx::tc_fence_after();
-        const uint32_t p = tmem + b * 2 * BN, ds = p + BN;
-        if (KEY) {
-          gradient(acc0, p, s + C::HALF_STAGE, j == 0);  // dV += P^T E
-          ptx::mma_commit(ptx::smem_u32(&sh->vdone[b]));
-          gradient(acc1, ds, s, j == 0);                 // dK += dS^T Q
-        } else {
-          gradient(acc0, ds, s, j == 0);                 // dQ += dS K
-        }
-        ptx::mma_commit(ptx::smem_u32(&sh->empty[st]));
-        return true;
-      };
-      bool ok = wait(sh->res, 0);
-      if (NBUF == 2 && ok) ok = scores(0);
-      for (int j = 0; j < n && ok; ++j) {
-        if (NBUF == 2) {
-          if (j + 1 < n) ok = scores(j + 1);
-        } else {
-          ok = scores(j);
-        }
-        ok = ok && grads(j);
+          ptx::mma_f16_on(on, d, ptx::sdesc_kmajor_sw128(r + c * BOX_BYTES + 32 * k),
+                          ptx::sdesc_kmajor_sw128(s + c * BOX_BYTES + 32 * k), id_s, (c | k) != 0);
+    };
+    // sum += (bf16 tile in TMEM) x (streamed tile read MN-major: 16 rows, 2048
+    // bytes, per step). The softmax warps of column half h left their 64
+    // columns at 64 h: four steps each.
+    auto gradient = [&](uint32_t acc, uint32_t p, uint32_t s, bool first) {
+      ptx::tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        ptx::mma_f16_ts_on(on, acc, p + 64 * (k >> 2) + 8 * (k & 3),
+                           ptx::sdesc_mnmajor_sw128(s + 2048 * k, BOX_BYTES), id_g,
+                           !first || k != 0);
+    };
+    auto wait = [&](uint64_t& bar, int use) {
+      return wait_warp(ptx::smem_u32(&bar), (uint32_t)use & 1u, abort, a.status);
+    };
+    auto commit = [&](uint64_t& bar) { ptx::mma_commit_on(on, ptx::smem_u32(&bar)); };
+    const uint32_t acc0 = tmem + C::ACC, acc1 = acc0 + D, dp = tmem + C::DP;
+    auto s0 = [&](int j) { return base + C::S0 + (uint32_t)((j % ST) * C::TILE_BYTES); };
+    auto s1 = [&](int j) { return base + C::S1 + (uint32_t)((j % ST) * C::TILE_BYTES); };
+    bool issued = false;
+    // Each product waits for its operands, and for what still reads the columns that
+    // it overwrites: `free` is a stage barrier of tile o (its gradient MMAs), o < 0: none.
+    auto s_product = [&](int j, uint64_t* free, int o) {
+      if (!wait(sh->full0[j % ST], j / ST)) return false;
+      if (o >= 0 && !wait(free[o % ST], o / ST)) return false;
+      product(tmem + (j % NS) * BN, base, s0(j));
+      commit(sh->sfull[j % NS]);
+      issued = true;
+      return true;
+    };
+    auto dp_product = [&](int j) {
+      if (!wait(sh->full1[j % ST], j / ST)) return false;
+      if (j > 0 && !wait(sh->empty0[(j - 1) % ST], (j - 1) / ST)) return false;
+      product(dp, base + C::TILE_BYTES, s1(j));
+      if (!KEY) commit(sh->empty1[j % ST]);
+      commit(sh->dpfull);
+      return true;
+    };
+    bool ok = wait(sh->res, 0) && s_product(0, nullptr, -1) && dp_product(0);
+    if (KEY && NS == 2 && n > 1) ok = ok && s_product(1, nullptr, -1);
+    for (int j = 0; j < n && ok; ++j) {
+      if (KEY) {
+        ok = wait(sh->pfull[j & 1], j >> 1);
+        if (!ok) break;
+        gradient(acc0, tmem + (j % NS) * BN, s1(j), j == 0);  // dV += P^T E
+        commit(sh->empty1[j % ST]);
+        if (j + NS < n) ok = s_product(j + NS, sh->empty1, j);
+      } else if (j + 1 < n) {
+        // (the softmax read this buffer's last scores before dS of tile j - 1)
+        ok = s_product(j + 1, nullptr, -1);
       }
-      if (issued) {
-        // all MMAs complete before the sums are read, or TMEM is released
-        ptx::mma_commit(ptx::smem_u32(&sh->afull));
-        int dummy = 0;
-        wait_bounded(ptx::smem_u32(&sh->afull), 0, &dummy, a.status);
-      }
+      ok = ok && wait(sh->dsfull, j);
+      if (!ok) break;
+      gradient(KEY ? acc1 : acc0, dp, s0(j), j == 0);         // dK += dS^T Q, dQ += dS K
+      commit(sh->empty0[j % ST]);
+      if (j + 1 < n) ok = dp_product(j + 1);
+    }
+    if (issued) {
+      // all MMAs complete before the sums are read, or TMEM is released
+      commit(sh->afull);
+      int dummy = 0;
+      wait_warp(ptx::smem_u32(&sh->afull), 0, &dummy, a.status);
     }
   } else {
     // ---------------- softmax warps 2..9 ----------------
@@ -370,82 +388,131 @@ __global__ __launch_bounds__(THREADS, D == 64 ? 2 : 1) void k_attn_exact_bwd_tc(
     const bool in = rr < len;
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
     const float c2 = a.scale * kLog2e;
-    float lse2 = inf_f(), delta = 0.0f;
+    // the other column half's thread of this row, through shared memory
+    auto row_sum = [&](float v) {
+      s_col[half * BM + row] = v;
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * SOFT_WARPS) : "memory");
+      return s_col[row] + s_col[BM + row];
+    };
+    float nlse2 = -inf_f(), ndelta = 0.0f;  // -lse (log2; p = 0 past the end), -delta
     if (!KEY) {
-      // delta = <o, e>: this thread's half of the row's columns
-      float d = 0.0f;
-      if (in) {
-        const int64_t r = beg + rr;
-        const uint4* o = reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.O_in + r * a.ldo +
-                                                        head * D + half * (D / 2));
-        const uint4* e = reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.E + r * a.lde +
-                                                        head * D + half * (D / 2));
+      if (in) nlse2 = -a.lse[(beg + rr) * a.H + head] * kLog2e;
+      if (tile > 0) {
+        // delta = <o, e>: this thread's half of the row's columns
+        float d = 0.0f;
+        if (in) {
+          const int64_t r = beg + rr;
+          const uint4* o = reinterpret_cast<const uint4*>(
+              (const __nv_bfloat16*)a.O_in + r * a.ldo + head * D + half * (D / 2));
+          const uint4* e = reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.E + r * a.lde +
+                                                          head * D + half * (D / 2));
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint4 x = __ldg(o + i), y = __ldg(e + i);
-          const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+          for (int i = 0; i < D / 16; ++i) {
+            const uint4 x = __ldg(o + i), y = __ldg(e + i);
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            d = fmaf(__uint_as_float(xs[w] << 16), __uint_as_float(ys[w] << 16), d);
-            d = fmaf(__uint_as_float(xs[w] & 0xffff0000u), __uint_as_float(ys[w] & 0xffff0000u), d);
+            for (int w = 0; w < 4; ++w) {
+              d = fmaf(__uint_as_float(xs[w] << 16), __uint_as_float(ys[w] << 16), d);
+              d = fmaf(__uint_as_float(xs[w] & 0xffff0000u),
+                       __uint_as_float(ys[w] & 0xffff0000u), d);
+            }
           }
         }
-        lse2 = a.lse[r * a.H + head] * kLog2e;
+        ndelta = -row_sum(d);
       }
-      s_col[half * BM + row] = d;
-      asm volatile("bar.sync 1, %0;" ::"n"(32 * SOFT_WARPS) : "memory");
-      delta = s_col[row] + s_col[BM + row];
-      if (in && half == 0) a.delta[(beg + rr) * a.H + head] = delta;
     }
-    bool ok = true;
+    bool ok = true, summed = KEY || tile > 0;
     for (int j = 0; j < n; ++j) {
-      const int b = j % NBUF, st = j % STAGES;
-      const int c0 = (s_off + j % per_head) * BN + 32 * half;  // first column's place
-      ok = wait_warp(ptx::smem_u32(&sh->sfull[b]), (uint32_t)(j / NBUF) & 1u, abort, a.status);
-      // (the producer's lse and delta are ordered by its own barrier)
-      if (KEY && ok)
-        ok = wait_warp(ptx::smem_u32(&sh->full[st]), (uint32_t)(j / STAGES) & 1u, abort, a.status);
-      if (!ok) break;
-      ptx::tc_fence_after();
-      const uint32_t ts = lane_base + b * 2 * BN + 32 * half, td = ts + BN;
-      uint32_t s[32], d[32];
-      ptx::tmem_ld32x2(ts, s, td, d);
-      // the tiles that cross the diagonal
-      const bool diag = KEY ? j % per_head < 2 : j >= 2 * tile;
-      uint32_t p16[16], d16[16];
-      const float* cl = s_col + st * 2 * BN + 32 * half;
+      const int b = j % NS, st = j % ST;
+      const float* cl = s_col + st * 2 * BN + 64 * half;
+      float2 p[32];
+      {  // P from S
+        // (the producer's lse and delta are ordered by its own barrier)
+        if (KEY)
+          ok = wait_warp(ptx::smem_u32(&sh->full0[st]), (uint32_t)(j / ST) & 1u, abort, a.status);
+        ok = ok &&
+             wait_warp(ptx::smem_u32(&sh->sfull[b]), (uint32_t)(j / NS) & 1u, abort, a.status);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t ts = lane_base + b * BN + 64 * half;
+        uint32_t s[2][32];
+        ptx::tmem_ld32x2(ts, s[0], ts + 32, s[1]);
+        if (j % per_head == (KEY ? 0 : tile)) {  // the tile on the diagonal: column > or < row
 #pragma unroll
-      for (int i = 0; i < 32; i += 4) {
-        float4 l4 = make_float4(lse2, lse2, lse2, lse2), d4 = make_float4(delta, delta, delta, delta);
+          for (int i = 0; i < 64; ++i)
+            if (KEY ? 64 * half + i < row : 64 * half + i > row)
+              s[i >> 5][i & 31] = 0xff800000u;  // -inf: p = 0
+        }
+        const float2 cc = make_float2(c2, c2);
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          float4 l4 = make_float4(nlse2, nlse2, nlse2, nlse2);
+          if (KEY) l4 = *reinterpret_cast<const float4*>(cl + 2 * i);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int e = 2 * (i + k);
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[e >> 5][e & 31]),
+                                                    __uint_as_float(s[e >> 5][(e & 31) + 1])),
+                                        cc, k ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y));
+            p[i + k] = make_float2(ex2(x.x), ex2(x.y));
+            if (KEY) pk[(i + k) & 15] = pack_bf16(p[i + k].x, p[i + k].y);
+          }
+          if (KEY && (i & 15) == 14) ptx::tmem_st16(ts + (i & 16), pk);
+        }
         if (KEY) {
-          l4 = *reinterpret_cast<const float4*>(cl + i);
-          d4 = *reinterpret_cast<const float4*>(cl + BN + i);
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh->pfull[j & 1]));
         }
-        const float ls[4] = {l4.x, l4.y, l4.z, l4.w}, dl[4] = {d4.x, d4.y, d4.z, d4.w};
-        float p[4], ds[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float x = fmaf(__uint_as_float(s[i + k]), c2, -ls[k]);
-          if (diag && (KEY ? c0 + i + k < rr : c0 + i + k > rr)) x = -inf_f();
-          p[k] = ex2(x);
-          ds[k] = p[k] * (__uint_as_float(d[i + k]) - dl[k]);
-        }
-        p16[i / 2] = pack_bf16(p[0], p[1]);
-        p16[i / 2 + 1] = pack_bf16(p[2], p[3]);
-        d16[i / 2] = pack_bf16(ds[0], ds[1]);
-        d16[i / 2 + 1] = pack_bf16(ds[2], ds[3]);
       }
-      if (KEY) ptx::tmem_st16(ts, p16);
-      ptx::tmem_st16(td, d16);
-      ptx::tmem_wait_st();
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh->pfull[b]));
+      {  // dS from P and dP
+        ok = wait_warp(ptx::smem_u32(&sh->dpfull), (uint32_t)j & 1u, abort, a.status);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t td = lane_base + C::DP + 64 * half;
+        uint32_t d[2][32];
+        ptx::tmem_ld32x2(td, d[0], td + 32, d[1]);
+        auto dpair = [&](int i) {
+          const int e = 2 * i;
+          return make_float2(__uint_as_float(d[e >> 5][e & 31]),
+                             __uint_as_float(d[e >> 5][(e & 31) + 1]));
+        };
+        if (!KEY && tile == 0) {  // one tile: delta = sum_j P dP, all at hand
+          float2 acc = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc = __ffma2_rn(p[i], dpair(i), acc);
+          ndelta = -row_sum(acc.x + acc.y);
+          summed = true;
+        }
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          float4 d4 = make_float4(ndelta, ndelta, ndelta, ndelta);
+          if (KEY) d4 = *reinterpret_cast<const float4*>(cl + BN + 2 * i);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float2 ds = __fmul2_rn(
+                p[i + k], __fadd2_rn(dpair(i + k), k ? make_float2(d4.z, d4.w)
+                                                     : make_float2(d4.x, d4.y)));
+            pk[(i + k) & 15] = pack_bf16(ds.x, ds.y);
+          }
+          if ((i & 15) == 14) ptx::tmem_st16(td + (i & 16), pk);
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh->dsfull));
+      }
     }
+    // (after an abort: the other warps do not wait for this one's part of delta)
+    if (!summed) asm volatile("bar.arrive 1, %0;" ::"n"(32 * SOFT_WARPS) : "memory");
+    if (!KEY && in && half == 0) a.delta[(beg + rr) * a.H + head] = -ndelta;
     if (ok) ok = wait_warp(ptx::smem_u32(&sh->afull), 0, abort, a.status);
     if (ok && !*abort) {
       ptx::tc_fence_after();
-      const uint32_t acc = lane_base + C::ACC_COL + half * (D / 2);
+      const uint32_t acc = lane_base + C::ACC + half * (D / 2);
       const int64_t r = beg + rr;
       const int64_t col = (int64_t)head * D + half * (D / 2);
       if (KEY) {
@@ -460,7 +527,7 @@ __global__ __launch_bounds__(THREADS, D == 64 ? 2 : 1) void k_attn_exact_bwd_tc(
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (warp == 1) ptx::tmem_dealloc(tmem, C::TMEM_COLS);
+  if (warp == 1) ptx::tmem_dealloc(tmem, 512);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -476,11 +543,11 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// T x cols bf16 rows (stride ld) as boxes of 64 columns x 64 rows, 128-byte swizzle.
+// T x cols bf16 rows (stride ld) as boxes of 64 columns x 128 rows, 128-byte swizzle.
 bool make_map(CUtensorMap* map, const void* p, int64_t T, int64_t cols, int64_t ld) {
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)T};
   const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {64, 64}, estr[2] = {1, 1};
+  const cuuint32_t box[2] = {64, BN}, estr[2] = {1, 1};
   return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides,
                      box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -492,14 +559,14 @@ cudaError_t launch_side(cudaStream_t st, const AttnArgs& a, const CUtensorMap& q
                         const CUtensorMap& e, const CUtensorMap& k, const CUtensorMap& v) {
   auto fn = k_attn_exact_bwd_tc<D, KEY>;
   const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)Cfg<D>::SMEM);
+                                               (int)Cfg<D, KEY>::SMEM);
   if (err != cudaSuccess) return err;
   const dim3 grid((unsigned)(KEY ? a.Hkv : a.H) * (unsigned)a.n_seqs,
                   (unsigned)((a.max_len + BM - 1) / BM));
   if (KEY)
-    fn<<<grid, THREADS, Cfg<D>::SMEM, st>>>(k, v, q, e, a);
+    fn<<<grid, THREADS, Cfg<D, KEY>::SMEM, st>>>(k, v, q, e, a);
   else
-    fn<<<grid, THREADS, Cfg<D>::SMEM, st>>>(q, e, k, v, a);
+    fn<<<grid, THREADS, Cfg<D, KEY>::SMEM, st>>>(q, e, k, v, a);
   return cudaGetLastError();
 }
 
