@@ -21,10 +21,12 @@
 //
 // Warp roles: warp 0 TMA producer, warp 1 MMA issuer, warps 2..9 softmax (two
 // warps per TMEM lane quarter, 64 of the tile's 128 columns each). The softmax of
-// a tile has two halves, P from S and dS from dP, and the MMAs are ordered so
-// that the tensor pipe works through both: S of the next tile runs while dS is
-// formed, the gradient products and the next dP while the next P is. Where TMEM
-// has room S has two buffers (all but the key side of 128-wide heads).
+// a tile has two halves, P from S and dS from dP. Where TMEM has room (all but
+// the key side of 128-wide heads) S has two buffers, and P and dS go over the
+// columns of the tile's S, which is dead by then: the next tile's P starts at
+// once, from scores that are already there, and the gradient products and the
+// next dP run under it. Else P goes over S and dS over dP, and the MMAs alternate
+// so that S of the next tile runs while dS is formed.
 //
 // delta = <o, e> is taken from the bf16 output o, whose rounding matters where
 // few keys average it out; in a sequence's first 128 rows the kernel sums
@@ -56,16 +58,20 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 template <int D, bool KEY>
 struct Cfg {
   static constexpr int NS = KEY && D == 128 ? 1 : 2;  // score buffers
-  static constexpr int STAGES = D == 128 ? 2 : 4;
+  static constexpr int ST0 = D == 64 ? 4 : (KEY ? 2 : 3);  // stages of either streamed tensor
+  static constexpr int ST1 = D == 64 ? 4 : 2;
   static constexpr int BOXES = D / 64;                // boxes per 128 rows of a tensor
   static constexpr int TILE_BYTES = BM * D * 2;       // 128 rows of a tensor
-  // shared memory: the resident tensors, then the stages of either streamed tensor
-  static constexpr int S0 = 2 * TILE_BYTES, S1 = S0 + STAGES * TILE_BYTES;
-  static constexpr int COL = S1 + STAGES * TILE_BYTES;  // -lse and -delta per stage
-  static constexpr int COL_BYTES = STAGES * 2 * BN * 4;
+  // shared memory: the resident tensors, the stages, then (key side) -lse and
+  // -delta per stage of s0 or (query side) partial deltas
+  static constexpr int S0 = 2 * TILE_BYTES, S1 = S0 + ST0 * TILE_BYTES;
+  static constexpr int COL = S1 + ST1 * TILE_BYTES;
+  static constexpr int COL_BYTES = (KEY ? ST0 : 1) * 2 * BN * 4;
   static constexpr size_t SMEM = 1024 + (size_t)COL + COL_BYTES + 256;
   // TMEM columns: score buffers, dP, the sums
   static constexpr int DP = NS * BN, ACC = DP + BN;
+  // where a column half's dS goes, from its S columns (NS 2) or its dP columns (NS 1)
+  static constexpr int DS = KEY && NS == 2 ? 32 : 0;
   static_assert(ACC + (KEY ? 2 : 1) * D <= 512, "TMEM columns");
   static_assert(SMEM <= 227 * 1024 && COL_BYTES >= 2 * BM * 4, "shared memory");
 };
@@ -151,7 +157,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
     const __grid_constant__ CUtensorMap tmS0, const __grid_constant__ CUtensorMap tmS1,
     AttnArgs a) {
   using C = Cfg<D, KEY>;
-  constexpr int NS = C::NS, ST = C::STAGES;
+  constexpr int NS = C::NS, ST0 = C::ST0, ST1 = C::ST1;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -184,7 +190,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
   if (threadIdx.x == 0) {
     ptx::mbar_init(ptx::smem_u32(&sh->res), 1);
     ptx::mbar_init(ptx::smem_u32(&sh->land), 1);
-    for (int s = 0; s < ST; ++s) {
+    for (int s = 0; s < 4; ++s) {
       ptx::mbar_init(ptx::smem_u32(&sh->full0[s]), 2);  // the bytes, and the producer's word
       ptx::mbar_init(ptx::smem_u32(&sh->full1[s]), 2);
       ptx::mbar_init(ptx::smem_u32(&sh->empty0[s]), 1);
@@ -237,10 +243,11 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
     uint32_t land_phase = 0;
     int armed0 = 0, armed1 = 0;  // tiles of s0 and s1 whose copies were issued
     // one tile of one streamed tensor into its stage; false after an abort
-    auto load = [&](const CUtensorMap* map, uint32_t off, uint64_t* full, uint64_t* empty, int j,
-                    int* armed) {
-      const int st = j % ST;
-      if (!wait_warp(ptx::smem_u32(&empty[st]), ((uint32_t)(j / ST) & 1u) ^ 1u, abort, a.status))
+    auto load = [&](const CUtensorMap* map, uint32_t off, int stages, uint64_t* full,
+                    uint64_t* empty, int j, int* armed) {
+      const int st = j % stages;
+      if (!wait_warp(ptx::smem_u32(&empty[st]), ((uint32_t)(j / stages) & 1u) ^ 1u, abort,
+                     a.status))
         return false;
       const int h = KEY ? head * group + j / per_head : head / group;
       const int r = (s_off + j % per_head) * BN;
@@ -284,24 +291,25 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
       return true;
     };
     for (int j = 0; j < n; ++j)
-      if (!load(&tmS0, C::S0, sh->full0, sh->empty0, j, &armed0) ||
-          !load(&tmS1, C::S1, sh->full1, sh->empty1, j, &armed1))
+      if (!load(&tmS0, C::S0, ST0, sh->full0, sh->empty0, j, &armed0) ||
+          !load(&tmS1, C::S1, ST1, sh->full1, sh->empty1, j, &armed1))
         break;
     // every copy has landed before the CTA can exit (after an abort the last
     // stages may not have been waited for by the MMAs)
     if (*abort) {
       int dummy = 0;
       wait_warp(ptx::smem_u32(&sh->res), 0, &dummy, a.status);
-      auto landed = [&](uint64_t* full, int armed) {
-        for (int j = max(0, armed - ST); j < armed; ++j) {
+      auto landed = [&](uint64_t* full, int stages, int armed) {
+        for (int j = max(0, armed - stages); j < armed; ++j) {
           if ((s_off + j % per_head) * BN + BN > len)
             wait_warp(ptx::smem_u32(&sh->land), land_phase, &dummy, a.status);
           else
-            wait_warp(ptx::smem_u32(&full[j % ST]), (uint32_t)(j / ST) & 1u, &dummy, a.status);
+            wait_warp(ptx::smem_u32(&full[j % stages]), (uint32_t)(j / stages) & 1u, &dummy,
+                      a.status);
         }
       };
-      landed(sh->full0, armed0);
-      landed(sh->full1, armed1);
+      landed(sh->full0, ST0, armed0);
+      landed(sh->full1, ST1, armed1);
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer (the warp together, lane 0 issues) ----------------
@@ -334,45 +342,55 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
     };
     auto commit = [&](uint64_t& bar) { ptx::mma_commit_on(on, ptx::smem_u32(&bar)); };
     const uint32_t acc0 = tmem + C::ACC, acc1 = acc0 + D, dp = tmem + C::DP;
-    auto s0 = [&](int j) { return base + C::S0 + (uint32_t)((j % ST) * C::TILE_BYTES); };
-    auto s1 = [&](int j) { return base + C::S1 + (uint32_t)((j % ST) * C::TILE_BYTES); };
+    auto s0 = [&](int j) { return base + C::S0 + (uint32_t)((j % ST0) * C::TILE_BYTES); };
+    auto s1 = [&](int j) { return base + C::S1 + (uint32_t)((j % ST1) * C::TILE_BYTES); };
+    auto s_at = [&](int j) { return tmem + (j % NS) * BN; };
+    // the gradient MMAs of tile j on s0 (dV's on s1) are complete
+    auto done0 = [&](int j) { return wait(sh->empty0[j % ST0], j / ST0); };
+    auto done1 = [&](int j) { return wait(sh->empty1[j % ST1], j / ST1); };
     bool issued = false;
-    // Each product waits for its operands, and for what still reads the columns that
-    // it overwrites: `free` is a stage barrier of tile o (its gradient MMAs), o < 0: none.
-    auto s_product = [&](int j, uint64_t* free, int o) {
-      if (!wait(sh->full0[j % ST], j / ST)) return false;
-      if (o >= 0 && !wait(free[o % ST], o / ST)) return false;
-      product(tmem + (j % NS) * BN, base, s0(j));
+    auto s_product = [&](int j) {
+      if (!wait(sh->full0[j % ST0], j / ST0)) return false;
+      product(s_at(j), base, s0(j));
       commit(sh->sfull[j % NS]);
       issued = true;
       return true;
     };
     auto dp_product = [&](int j) {
-      if (!wait(sh->full1[j % ST], j / ST)) return false;
-      if (j > 0 && !wait(sh->empty0[(j - 1) % ST], (j - 1) / ST)) return false;
+      if (!wait(sh->full1[j % ST1], j / ST1)) return false;
       product(dp, base + C::TILE_BYTES, s1(j));
-      if (!KEY) commit(sh->empty1[j % ST]);
+      if (!KEY) commit(sh->empty1[j % ST1]);
       commit(sh->dpfull);
       return true;
     };
-    bool ok = wait(sh->res, 0) && s_product(0, nullptr, -1) && dp_product(0);
-    if (KEY && NS == 2 && n > 1) ok = ok && s_product(1, nullptr, -1);
+    auto dv_product = [&](int j) {  // dV += P^T E
+      if (!wait(sh->pfull[j & 1], j >> 1)) return false;
+      gradient(acc0, s_at(j), s1(j), j == 0);
+      commit(sh->empty1[j % ST1]);
+      return true;
+    };
+    auto ds_product = [&](int j) {  // dK += dS^T Q, dQ += dS K
+      gradient(KEY ? acc1 : acc0, (NS == 2 ? s_at(j) : dp) + C::DS, s0(j), j == 0);
+      commit(sh->empty0[j % ST0]);
+    };
+    bool ok = wait(sh->res, 0) && s_product(0) && dp_product(0);
+    if (NS == 2 && n > 1) ok = ok && s_product(1);
     for (int j = 0; j < n && ok; ++j) {
-      if (KEY) {
-        ok = wait(sh->pfull[j & 1], j >> 1);
+      if (KEY) ok = dv_product(j);
+      if (NS == 2) {
+        // dP's columns are read (dS is there); S's are free after this tile's MMAs
+        ok = ok && wait(sh->dsfull, j) && (j + 1 == n || dp_product(j + 1));
         if (!ok) break;
-        gradient(acc0, tmem + (j % NS) * BN, s1(j), j == 0);  // dV += P^T E
-        commit(sh->empty1[j % ST]);
-        if (j + NS < n) ok = s_product(j + NS, sh->empty1, j);
-      } else if (j + 1 < n) {
-        // (the softmax read this buffer's last scores before dS of tile j - 1)
-        ok = s_product(j + 1, nullptr, -1);
+        ds_product(j);
+        if (j + 2 < n) ok = done0(j) && s_product(j + 2);
+      } else {
+        // S's columns are free after dV's MMAs, dP's after dK's
+        if (j + 1 < n) ok = ok && done1(j) && s_product(j + 1);
+        ok = ok && wait(sh->dsfull, j);
+        if (!ok) break;
+        ds_product(j);
+        if (j + 1 < n) ok = done0(j) && dp_product(j + 1);
       }
-      ok = ok && wait(sh->dsfull, j);
-      if (!ok) break;
-      gradient(KEY ? acc1 : acc0, dp, s0(j), j == 0);         // dK += dS^T Q, dQ += dS K
-      commit(sh->empty0[j % ST]);
-      if (j + 1 < n) ok = dp_product(j + 1);
     }
     if (issued) {
       // all MMAs complete before the sums are read, or TMEM is released
@@ -423,18 +441,18 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
     }
     bool ok = true, summed = KEY || tile > 0;
     for (int j = 0; j < n; ++j) {
-      const int b = j % NS, st = j % ST;
+      const int b = j % NS, st = j % ST0;
+      const uint32_t ts = lane_base + b * BN + 64 * half;
       const float* cl = s_col + st * 2 * BN + 64 * half;
       float2 p[32];
       {  // P from S
         // (the producer's lse and delta are ordered by its own barrier)
         if (KEY)
-          ok = wait_warp(ptx::smem_u32(&sh->full0[st]), (uint32_t)(j / ST) & 1u, abort, a.status);
+          ok = wait_warp(ptx::smem_u32(&sh->full0[st]), (uint32_t)(j / ST0) & 1u, abort, a.status);
         ok = ok &&
              wait_warp(ptx::smem_u32(&sh->sfull[b]), (uint32_t)(j / NS) & 1u, abort, a.status);
         if (!ok) break;
         ptx::tc_fence_after();
-        const uint32_t ts = lane_base + b * BN + 64 * half;
         uint32_t s[2][32];
         ptx::tmem_ld32x2(ts, s[0], ts + 32, s[1]);
         if (j % per_head == (KEY ? 0 : tile)) {  // the tile on the diagonal: column > or < row
@@ -498,7 +516,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
                                                      : make_float2(d4.x, d4.y)));
             pk[(i + k) & 15] = pack_bf16(ds.x, ds.y);
           }
-          if ((i & 15) == 14) ptx::tmem_st16(td + (i & 16), pk);
+          if ((i & 15) == 14) ptx::tmem_st16((NS == 2 ? ts : td) + C::DS + (i & 16), pk);
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
