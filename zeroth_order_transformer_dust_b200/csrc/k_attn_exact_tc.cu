@@ -16,11 +16,13 @@
 // the CTA's whole life. Rounding P and dS to bf16 (half a step, 2^-8 relative,
 // per term, against fp32 sums) is what puts their products on the tensor cores.
 //
-// Tiles of 128 and not 64 streamed rows: a 128 x 64 x 16 MMA takes as long as a
-// 128 x 128 x 16 one (64 cycles: its A operand is read at the same rate).
+// Tiles of 128 and not 64 streamed rows: a 128 x 64 x 16 product takes 47 cycles
+// where a 128 x 128 x 16 one takes 62 (its A operand is read at the same rate),
+// and the hand-overs between the warps, about 150 cycles each, come half as often.
 //
-// Warp roles: warp 0 TMA producer, warp 1 MMA issuer, warps 2..9 softmax (two
-// warps per TMEM lane quarter, 64 of the tile's 128 columns each). The softmax of
+// Warp roles: warp 0 TMA producer, warp 1 issues the score products, warp 10 the
+// gradient products (one thread for both spends more time between its waits
+// than the tensor pipe does on the MMAs), warps 2..9 softmax (two warps per TMEM lane quarter, 64 of the tile's 128 columns each). The softmax of
 // a tile has two halves, P from S and dS from dP. Where TMEM has room (all but
 // the key side of 128-wide heads) S has two buffers, and P and dS go over the
 // columns of the tile's S, which is dead by then: the next tile's P starts at
@@ -51,7 +53,7 @@ constexpr int BM = 128;  // resident rows: TMEM lanes
 constexpr int BN = 128;  // rows of a streamed tile
 constexpr int BOX_BYTES = 128 * 64 * 2;  // a TMA box: 128 rows x 64 columns
 constexpr int SOFT_WARPS = 8;
-constexpr int THREADS = 64 + 32 * SOFT_WARPS;
+constexpr int THREADS = 96 + 32 * SOFT_WARPS;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
@@ -77,8 +79,8 @@ struct Cfg {
 };
 
 struct Bars {
-  uint64_t res, land, full0[4], full1[4], empty0[4], empty1[4], sfull[2], pfull[2], dpfull, dsfull,
-      afull;
+  uint64_t res, land, full0[4], full1[4], empty0[4], empty1[4], sfull[2], pfull[2], dsfull[2], dpfull,
+      vdone, sdone, afull;
   uint32_t tmem_base;
   int abort;
 };
@@ -199,9 +201,11 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(ptx::smem_u32(&sh->sfull[b]), 1);
       ptx::mbar_init(ptx::smem_u32(&sh->pfull[b]), SOFT_WARPS);
+      ptx::mbar_init(ptx::smem_u32(&sh->dsfull[b]), SOFT_WARPS);
     }
     ptx::mbar_init(ptx::smem_u32(&sh->dpfull), 1);
-    ptx::mbar_init(ptx::smem_u32(&sh->dsfull), SOFT_WARPS);
+    ptx::mbar_init(ptx::smem_u32(&sh->vdone), 1);
+    ptx::mbar_init(ptx::smem_u32(&sh->sdone), 1);
     ptx::mbar_init(ptx::smem_u32(&sh->afull), 1);
     sh->abort = 0;
     ptx::fence_barrier_init();
@@ -222,6 +226,10 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
+  // by one thread: use `use` of a barrier
+  auto wait = [&](uint64_t& bar, int use) {
+    return wait_bounded(ptx::smem_u32(&bar), (uint32_t)use & 1u, abort, a.status);
+  };
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
@@ -312,91 +320,89 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
       landed(sh->full1, ST1, armed1);
     }
   } else if (warp == 1) {
-    // ---------------- MMA issuer (the warp together, lane 0 issues) ----------------
-    constexpr uint32_t id_s = ptx::idesc_bf16_f32(BM, BN);
-    constexpr uint32_t id_g = ptx::idesc_bf16_f32(BM, D) | ptx::kIdescBMn;
-    const uint32_t on = lane == 0;
-    // S or dP: K-major operands, 64-column boxes, 32 bytes per 16-deep step
-    auto product = [&](uint32_t d, uint32_t r, uint32_t s) {
-      ptx::tc_fence_after();
+    // ---------------- score products: S and dP ----------------
+    if (lane == 0) {
+      constexpr uint32_t id = ptx::idesc_bf16_f32(BM, BN);
+      // K-major operands, 64-column boxes, 32 bytes per 16-deep step
+      auto product = [&](uint32_t d, uint32_t r, uint32_t s) {
+        ptx::tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < C::BOXES; ++c)
+        for (int c = 0; c < C::BOXES; ++c)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          ptx::mma_f16_on(on, d, ptx::sdesc_kmajor_sw128(r + c * BOX_BYTES + 32 * k),
-                          ptx::sdesc_kmajor_sw128(s + c * BOX_BYTES + 32 * k), id_s, (c | k) != 0);
-    };
-    // sum += (bf16 tile in TMEM) x (streamed tile read MN-major: 16 rows, 2048
-    // bytes, per step). The softmax warps of column half h left their 64
-    // columns at 64 h: four steps each.
-    auto gradient = [&](uint32_t acc, uint32_t p, uint32_t s, bool first) {
-      ptx::tc_fence_after();
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        ptx::mma_f16_ts_on(on, acc, p + 64 * (k >> 2) + 8 * (k & 3),
-                           ptx::sdesc_mnmajor_sw128(s + 2048 * k, BOX_BYTES), id_g,
-                           !first || k != 0);
-    };
-    auto wait = [&](uint64_t& bar, int use) {
-      return wait_warp(ptx::smem_u32(&bar), (uint32_t)use & 1u, abort, a.status);
-    };
-    auto commit = [&](uint64_t& bar) { ptx::mma_commit_on(on, ptx::smem_u32(&bar)); };
-    const uint32_t acc0 = tmem + C::ACC, acc1 = acc0 + D, dp = tmem + C::DP;
-    auto s0 = [&](int j) { return base + C::S0 + (uint32_t)((j % ST0) * C::TILE_BYTES); };
-    auto s1 = [&](int j) { return base + C::S1 + (uint32_t)((j % ST1) * C::TILE_BYTES); };
-    auto s_at = [&](int j) { return tmem + (j % NS) * BN; };
-    // the gradient MMAs of tile j on s0 (dV's on s1) are complete
-    auto done0 = [&](int j) { return wait(sh->empty0[j % ST0], j / ST0); };
-    auto done1 = [&](int j) { return wait(sh->empty1[j % ST1], j / ST1); };
-    bool issued = false;
-    auto s_product = [&](int j) {
-      if (!wait(sh->full0[j % ST0], j / ST0)) return false;
-      product(s_at(j), base, s0(j));
-      commit(sh->sfull[j % NS]);
-      issued = true;
-      return true;
-    };
-    auto dp_product = [&](int j) {
-      if (!wait(sh->full1[j % ST1], j / ST1)) return false;
-      product(dp, base + C::TILE_BYTES, s1(j));
-      if (!KEY) commit(sh->empty1[j % ST1]);
-      commit(sh->dpfull);
-      return true;
-    };
-    auto dv_product = [&](int j) {  // dV += P^T E
-      if (!wait(sh->pfull[j & 1], j >> 1)) return false;
-      gradient(acc0, s_at(j), s1(j), j == 0);
-      commit(sh->empty1[j % ST1]);
-      return true;
-    };
-    auto ds_product = [&](int j) {  // dK += dS^T Q, dQ += dS K
-      gradient(KEY ? acc1 : acc0, (NS == 2 ? s_at(j) : dp) + C::DS, s0(j), j == 0);
-      commit(sh->empty0[j % ST0]);
-    };
-    bool ok = wait(sh->res, 0) && s_product(0) && dp_product(0);
-    if (NS == 2 && n > 1) ok = ok && s_product(1);
-    for (int j = 0; j < n && ok; ++j) {
-      if (KEY) ok = dv_product(j);
-      if (NS == 2) {
-        // dP's columns are read (dS is there); S's are free after this tile's MMAs
-        ok = ok && wait(sh->dsfull, j) && (j + 1 == n || dp_product(j + 1));
-        if (!ok) break;
-        ds_product(j);
-        if (j + 2 < n) ok = done0(j) && s_product(j + 2);
-      } else {
-        // S's columns are free after dV's MMAs, dP's after dK's
-        if (j + 1 < n) ok = ok && done1(j) && s_product(j + 1);
-        ok = ok && wait(sh->dsfull, j);
-        if (!ok) break;
-        ds_product(j);
-        if (j + 1 < n) ok = done0(j) && dp_product(j + 1);
+          for (int k = 0; k < 4; ++k)
+            ptx::mma_f16(d, ptx::sdesc_kmajor_sw128(r + c * BOX_BYTES + 32 * k),
+                         ptx::sdesc_kmajor_sw128(s + c * BOX_BYTES + 32 * k), id, (c | k) != 0);
+      };
+      bool issued = false;
+      auto s_product = [&](int j) {
+        if (!wait(sh->full0[j % ST0], j / ST0)) return false;
+        product(tmem + (j % NS) * BN, base, base + C::S0 + (j % ST0) * C::TILE_BYTES);
+        ptx::mma_commit(ptx::smem_u32(&sh->sfull[j % NS]));
+        issued = true;
+        return true;
+      };
+      auto dp_product = [&](int j) {
+        if (!wait(sh->full1[j % ST1], j / ST1)) return false;
+        product(tmem + C::DP, base + C::TILE_BYTES, base + C::S1 + (j % ST1) * C::TILE_BYTES);
+        ptx::mma_commit(ptx::smem_u32(&sh->dpfull));
+        if (!KEY) ptx::mma_commit(ptx::smem_u32(&sh->empty1[j % ST1]));
+        return true;
+      };
+      // the gradient MMAs of tile j are complete
+      auto done0 = [&](int j) { return wait(sh->empty0[j % ST0], j / ST0); };
+      bool ok = wait(sh->res, 0) && s_product(0) && dp_product(0);
+      if (NS == 2 && n > 1) ok = ok && s_product(1);
+      for (int j = 0; j + 1 < n && ok; ++j) {
+        if (NS == 2)  // dP's columns are read once dS is there; S's free after the tile's MMAs
+          ok = wait(sh->dsfull[j & 1], j >> 1) && dp_product(j + 1) &&
+               (j + 2 >= n || (done0(j) && s_product(j + 2)));
+        else          // S's columns are free after dV's MMAs, dP's after dK's
+          ok = wait(sh->vdone, j) && s_product(j + 1) && done0(j) && dp_product(j + 1);
+      }
+      if (issued) {  // complete before TMEM is released
+        int dummy = 0;
+        ptx::mma_commit(ptx::smem_u32(&sh->sdone));
+        wait_bounded(ptx::smem_u32(&sh->sdone), 0, &dummy, a.status);
       }
     }
-    if (issued) {
-      // all MMAs complete before the sums are read, or TMEM is released
-      commit(sh->afull);
-      int dummy = 0;
-      wait_warp(ptx::smem_u32(&sh->afull), 0, &dummy, a.status);
+  } else if (warp == 2 + SOFT_WARPS) {
+    // ---------------- gradient products ----------------
+    if (lane == 0) {
+      constexpr uint32_t id = ptx::idesc_bf16_f32(BM, D) | ptx::kIdescBMn;
+      // sum += (bf16 tile in TMEM) x (streamed tile read MN-major: 16 rows, 2048
+      // bytes, per step). The softmax warps of column half h left their 64
+      // columns at 64 h: four steps each.
+      auto gradient = [&](uint32_t acc, uint32_t p, uint32_t s, bool first) {
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          ptx::mma_f16_ts(acc, p + 64 * (k >> 2) + 8 * (k & 3),
+                          ptx::sdesc_mnmajor_sw128(s + 2048 * k, BOX_BYTES), id, !first || k != 0);
+      };
+      const uint32_t acc0 = tmem + C::ACC, acc1 = acc0 + D;
+      bool issued = false;
+      for (int j = 0; j < n; ++j) {
+        const uint32_t s_at = tmem + (j % NS) * BN;
+        // (P needs only s0's tile: s1's is waited for here, too)
+        if (KEY) {  // dV += P^T E
+          if (!wait(sh->full1[j % ST1], j / ST1) || !wait(sh->pfull[j & 1], j >> 1)) break;
+          gradient(acc0, s_at, base + C::S1 + (j % ST1) * C::TILE_BYTES, j == 0);
+          ptx::mma_commit(ptx::smem_u32(&sh->vdone));
+          issued = true;
+        }
+        // dK += dS^T Q, dQ += dS K; dS also means that dP's MMAs are done with s1's tile
+        if (!wait(sh->full0[j % ST0], j / ST0) || !wait(sh->dsfull[j & 1], j >> 1)) break;
+        gradient(KEY ? acc1 : acc0, (NS == 2 ? s_at : tmem + C::DP) + C::DS,
+                 base + C::S0 + (j % ST0) * C::TILE_BYTES, j == 0);
+        ptx::mma_commit(ptx::smem_u32(&sh->empty0[j % ST0]));
+        if (KEY) ptx::mma_commit(ptx::smem_u32(&sh->empty1[j % ST1]));
+        issued = true;
+      }
+      if (issued) {  // complete before the sums are read, or TMEM is released
+        int dummy = 0;
+        ptx::mma_commit(ptx::smem_u32(&sh->afull));
+        wait_bounded(ptx::smem_u32(&sh->afull), 0, &dummy, a.status);
+      }
     }
   } else {
     // ---------------- softmax warps 2..9 ----------------
@@ -521,7 +527,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh->dsfull));
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh->dsfull[j & 1]));
       }
     }
     // (after an abort: the other warps do not wait for this one's part of delta)
