@@ -1144,7 +1144,7 @@ dust_status dust_attn_forward(dust_ctx* ctx, const dust_attn_dims* dims, const v
   a.status = ctx->d_status;
   mark(ctx, nullptr);
   DUST_CU(ctx->tc_enabled && attn_exact_tc_supported(a, false)
-              ? launch_attn_exact_tc(ctx->stream, a, false)
+              ? launch_attn_fwd_tc(ctx->stream, a)
               : launch_attn_exact_simt(ctx->stream, a, false));
   ctx->launches += 1;
   mark(ctx, "attn_forward");
@@ -1177,7 +1177,7 @@ dust_status dust_attn_backward(dust_ctx* ctx, const dust_attn_dims* dims, const 
   a.status = ctx->d_status;
   mark(ctx, nullptr);
   DUST_CU(ctx->tc_enabled && attn_exact_tc_supported(a, true)
-              ? launch_attn_exact_tc(ctx->stream, a, true)
+              ? launch_attn_bwd_tc(ctx->stream, a)
               : launch_attn_exact_simt(ctx->stream, a, true));
   ctx->launches += 2;
   mark(ctx, "attn_backward");

@@ -437,7 +437,7 @@ cudaError_t launch_distill(cudaStream_t st, const void* Z, int dtype, int64_t T,
                            const float* weights, float* loss, void* dZ, int64_t ldg, int sm_count,
                            uint32_t* status);
 
-// Exact causal attention (k_attn_exact.cu, k_attn_exact_tc.cu): heads in columns
+// Exact causal attention (k_attn_exact.cu, k_attn_fwd_tc.cu, k_attn_bwd_tc.cu): heads in columns
 // [h head_dim, (h+1) head_dim) of rows with the given strides (elements).
 struct AttnArgs {
   const void *Q, *K, *V, *O_in, *E;  // O_in, E: backward
@@ -468,6 +468,7 @@ __device__ __forceinline__ bool attn_sequence(const AttnArgs& a, int seq, int64_
 cudaError_t launch_attn_exact_simt(cudaStream_t st, const AttnArgs& a, bool backward);
 // Tensor cores: bf16 rows on 16-byte boundaries, head_dim 64 or 128.
 bool attn_exact_tc_supported(const AttnArgs& a, bool backward);
-cudaError_t launch_attn_exact_tc(cudaStream_t st, const AttnArgs& a, bool backward);
+cudaError_t launch_attn_fwd_tc(cudaStream_t st, const AttnArgs& a);
+cudaError_t launch_attn_bwd_tc(cudaStream_t st, const AttnArgs& a);
 
 }  // namespace dust

@@ -1,0 +1,352 @@
+// Causal attention on tensor cores (bf16 tensors, 64- or 128-wide heads): the
+// forward pass of the exact attention; formulas as in k_attn_exact.cu.
+//
+// A CTA owns 256 query rows of a head as two tiles of 128 and streams key/value
+// tiles of 128 rows. Per streamed tile and query tile g, with the query rows as
+// TMEM lanes: S_g = Q_g K^T, P_g = exp2(S_g c - m_g) -> bf16 over S_g's TMEM
+// columns, O_g += P_g V with P_g taken from TMEM. While one tile's rows are in
+// softmax the tensor pipe works for the other. Bound by the exponentials as
+// much as by the MMAs: a 128 x 128 tile takes 1024 cycles of either with
+// 128-wide heads.
+//
+// One thread has one row, so no maximum crosses threads. The maximum that P is
+// taken against is only moved when a row's has grown by more than 8 (log2): P
+// then stays below 2^8, which costs a float nothing, and O, which lives in TMEM,
+// is rescaled in the few tiles where that happens instead of in every one. The
+// sum l is taken over the unrounded P; rounding P to bf16 for the product (half
+// a step, 2^-8 relative, per term) is what puts it on the tensor cores.
+//
+// Warp roles: warp 0 TMA producer, warp 1 issues S products, warp 2 the PV
+// products, warps 4..7 and 8..11 are the softmax of either query tile. Rows past
+// a sequence's end and bounded waits as in k_attn_bwd_tc.cu.
+#include "attn_tc.cuh"
+
+namespace dust {
+namespace {
+
+constexpr int THREADS = 128 + 32 * SOFT_WARPS;
+constexpr float kGrow = 8.0f;  // log2 growth of a row's maximum that rescales O
+
+template <int D>
+struct Cfg {
+  static constexpr int STK = D == 64 ? 4 : 3, STV = D == 64 ? 4 : 2;  // key, value stages
+  static constexpr int BOXES = D / 64;
+  static constexpr int TILE_BYTES = BM * D * 2;
+  static constexpr int K0 = 2 * TILE_BYTES, V0 = K0 + STK * TILE_BYTES;
+  static constexpr int BARS = V0 + STV * TILE_BYTES;
+  static constexpr size_t SMEM = 1024 + (size_t)BARS + 256;
+  static constexpr int O = 2 * BN;  // TMEM: S_0, S_1, O_0, O_1
+  static_assert(O + 2 * D <= 512, "TMEM columns");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+struct Bars {
+  uint64_t res[2], land, kfull[4], vfull[4], kempty[4], vempty[4], sfull[2], pfull[2], odone[2],
+      sdone, pvdone;
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(Bars) <= 256, "barrier block");
+
+template <int D>
+__global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
+    const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+    const __grid_constant__ CUtensorMap tmV, AttnArgs a) {
+  using C = Cfg<D>;
+  constexpr int STK = C::STK, STV = C::STV;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = ptx::smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* basep = smem_raw + (base - raw);
+  Bars* sh = reinterpret_cast<Bars*>(basep + C::BARS);
+  volatile int* abort = &sh->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  const int head = (int)(blockIdx.x % a.H), seq = (int)(blockIdx.x / a.H);
+  const int hk = head / (a.H / a.Hkv);
+  const int tile = (int)(gridDim.y - 1 - blockIdx.y);  // the longest rows first
+  int64_t beg, end;
+  if (!attn_sequence(a, seq, &beg, &end)) {
+    if (threadIdx.x == 0) atomicOr(a.status, kStatusBadSeq);
+    return;
+  }
+  const int len = (int)(end - beg);
+  const int r_first = 2 * tile * BM;
+  if (r_first >= len) return;
+  // key tiles up to the diagonal; the second query tile may lie past the end
+  const int n0 = 2 * tile + 1, n1 = r_first + BM < len ? 2 * tile + 2 : 0;
+  const int n = max(n0, n1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 4; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&sh->kfull[s]), 2);  // the bytes, and the producer's word
+      ptx::mbar_init(ptx::smem_u32(&sh->vfull[s]), 2);
+      ptx::mbar_init(ptx::smem_u32(&sh->kempty[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&sh->vempty[s]), 1);
+    }
+    for (int g = 0; g < 2; ++g) {
+      ptx::mbar_init(ptx::smem_u32(&sh->res[g]), 1);
+      ptx::mbar_init(ptx::smem_u32(&sh->sfull[g]), 1);
+      ptx::mbar_init(ptx::smem_u32(&sh->pfull[g]), SOFT_WARPS / 2);
+      ptx::mbar_init(ptx::smem_u32(&sh->odone[g]), 1);
+    }
+    ptx::mbar_init(ptx::smem_u32(&sh->land), 1);
+    ptx::mbar_init(ptx::smem_u32(&sh->sdone), 1);
+    ptx::mbar_init(ptx::smem_u32(&sh->pvdone), 1);
+    sh->abort = 0;
+    ptx::fence_barrier_init();
+    ptx::fence_proxy_async();
+    // the query rows are on their way while TMEM is allocated
+    for (int g = 0; g < (n1 ? 2 : 1); ++g) {
+      const uint32_t bar = ptx::smem_u32(&sh->res[g]);
+      ptx::mbar_expect_tx(bar, C::TILE_BYTES);
+      for (int c = 0; c < C::BOXES; ++c)
+        ptx::tma_load_2d(base + g * C::TILE_BYTES + c * BOX_BYTES, &tmQ, head * D + 64 * c,
+                         (int)(beg + r_first + g * BM), bar);
+    }
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_u32(&sh->tmem_base), 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+  // by one thread: use `use` of a barrier
+  auto wait = [&](uint64_t& bar, int use) {
+    return wait_bounded(ptx::smem_u32(&bar), (uint32_t)use & 1u, abort, a.status);
+  };
+
+  if (warp == 0) {
+    // ---------------- TMA producer ----------------
+    uint32_t land_phase = 0;
+    int armed_k = 0, armed_v = 0;  // tiles whose copies were issued
+    auto load = [&](const CUtensorMap* map, uint32_t off, int stages, uint64_t* full,
+                    uint64_t* empty, int j, int* armed) {
+      const int st = j % stages;
+      if (!wait_warp(ptx::smem_u32(&empty[st]), ((uint32_t)(j / stages) & 1u) ^ 1u, abort,
+                     a.status))
+        return false;
+      const uint32_t fb = ptx::smem_u32(&full[st]), land = ptx::smem_u32(&sh->land);
+      const bool partial = (j + 1) * BN > len;
+      if (lane == 0) {
+        const uint32_t bar = partial ? land : fb;
+        ptx::mbar_expect_tx(bar, C::TILE_BYTES);
+        for (int c = 0; c < C::BOXES; ++c)
+          ptx::tma_load_2d(base + off + st * C::TILE_BYTES + c * BOX_BYTES, map, hk * D + 64 * c,
+                           (int)(beg + j * BN), bar);
+      }
+      *armed = j + 1;
+      if (partial) {
+        if (!wait_warp(land, land_phase, abort, a.status)) return false;
+        land_phase ^= 1u;
+        zero_rows<D>(basep + off + st * C::TILE_BYTES, (j + 1) * BN - len, lane);
+      }
+      __syncwarp();
+      if (lane == 0) {
+        if (partial) ptx::mbar_arrive(fb);
+        ptx::mbar_arrive(fb);
+      }
+      return true;
+    };
+    for (int j = 0; j < n; ++j)
+      if (!load(&tmK, C::K0, STK, sh->kfull, sh->kempty, j, &armed_k) ||
+          !load(&tmV, C::V0, STV, sh->vfull, sh->vempty, j, &armed_v))
+        break;
+    // every copy has landed before the CTA can exit (after an abort the last
+    // stages may not have been waited for by the MMAs)
+    if (*abort) {
+      int dummy = 0;
+      for (int g = 0; g < (n1 ? 2 : 1); ++g)
+        wait_warp(ptx::smem_u32(&sh->res[g]), 0, &dummy, a.status);
+      auto landed = [&](uint64_t* full, int stages, int armed) {
+        for (int j = max(0, armed - stages); j < armed; ++j) {
+          if ((j + 1) * BN > len)
+            wait_warp(ptx::smem_u32(&sh->land), land_phase, &dummy, a.status);
+          else
+            wait_warp(ptx::smem_u32(&full[j % stages]), (uint32_t)(j / stages) & 1u, &dummy,
+                      a.status);
+        }
+      };
+      landed(sh->kfull, STK, armed_k);
+      landed(sh->vfull, STV, armed_v);
+    }
+  } else if (warp == 1) {
+    // ---------------- S_g = Q_g K^T ----------------
+    if (lane == 0) {
+      constexpr uint32_t id = ptx::idesc_bf16_f32(BM, BN);
+      bool issued = false, ok = true;
+      for (int j = 0; j < n && ok; ++j) {
+        ok = wait(sh->kfull[j % STK], j / STK);
+        for (int g = 0; g < 2 && ok; ++g) {
+          if (j >= (g ? n1 : n0)) continue;
+          // P of the previous tile lies over S: its product is complete
+          ok = j == 0 ? wait(sh->res[g], 0) : wait(sh->odone[g], j - 1);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t q = base + g * C::TILE_BYTES;
+          const uint32_t k = base + C::K0 + (j % STK) * C::TILE_BYTES;
+#pragma unroll
+          for (int c = 0; c < C::BOXES; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              ptx::mma_f16(tmem + g * BN, ptx::sdesc_kmajor_sw128(q + c * BOX_BYTES + 32 * i),
+                           ptx::sdesc_kmajor_sw128(k + c * BOX_BYTES + 32 * i), id, (c | i) != 0);
+          ptx::mma_commit(ptx::smem_u32(&sh->sfull[g]));
+          issued = true;
+        }
+        if (ok) ptx::mma_commit(ptx::smem_u32(&sh->kempty[j % STK]));
+      }
+      if (issued) {  // complete before TMEM is released
+        int dummy = 0;
+        ptx::mma_commit(ptx::smem_u32(&sh->sdone));
+        wait_bounded(ptx::smem_u32(&sh->sdone), 0, &dummy, a.status);
+      }
+    }
+  } else if (warp == 2) {
+    // ---------------- O_g += P_g V ----------------
+    if (lane == 0) {
+      constexpr uint32_t id = ptx::idesc_bf16_f32(BM, D) | ptx::kIdescBMn;
+      bool ok = true;
+      for (int j = 0; j < n && ok; ++j) {
+        ok = wait(sh->vfull[j % STV], j / STV);
+        for (int g = 0; g < 2 && ok; ++g) {
+          if (j >= (g ? n1 : n0)) continue;
+          ok = wait(sh->pfull[g], j);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t v = base + C::V0 + (j % STV) * C::TILE_BYTES;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            ptx::mma_f16_ts(tmem + C::O + g * D, tmem + g * BN + 8 * i,
+                            ptx::sdesc_mnmajor_sw128(v + 2048 * i, BOX_BYTES), id, (j | i) != 0);
+          ptx::mma_commit(ptx::smem_u32(&sh->odone[g]));
+        }
+        if (ok) ptx::mma_commit(ptx::smem_u32(&sh->vempty[j % STV]));
+      }
+      int dummy = 0;  // complete before TMEM is released
+      ptx::mma_commit(ptx::smem_u32(&sh->pvdone));
+      wait_bounded(ptx::smem_u32(&sh->pvdone), 0, &dummy, a.status);
+    }
+  } else if (warp >= 4) {
+    // ---------------- softmax ----------------
+    const int g = (warp - 4) >> 2, quad = warp & 3;
+    const int row = quad * 32 + lane;                  // TMEM lane
+    const int rr = r_first + g * BM + row;             // the row's place in the sequence
+    const int ng = g ? n1 : n0;
+    const bool in = rr < len;
+    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t ts = lane_base + g * BN, to = lane_base + C::O + g * D;
+    const float c2 = a.scale * kLog2e;
+    float m = 0.0f, l = 0.0f;
+    bool ok = true;
+    for (int j = 0; j < ng; ++j) {
+      ok = wait_warp(ptx::smem_u32(&sh->sfull[g]), (uint32_t)j & 1u, abort, a.status);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      const bool diag = j == ng - 1;
+      uint32_t s[2][32];
+      // 64 columns of S; on the diagonal tile keys past the row's are -inf
+      auto load = [&](int h) {
+        ptx::tmem_ld32x2(ts + 64 * h, s[0], ts + 64 * h + 32, s[1]);
+        if (diag) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (64 * h + i > row) s[i >> 5][i & 31] = 0xff800000u;
+        }
+      };
+      float mx[4] = {-inf_f(), -inf_f(), -inf_f(), -inf_f()};
+#pragma unroll
+      for (int h = 1; h >= 0; --h) {
+        load(h);
+#pragma unroll
+        for (int i = 0; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i >> 5][i & 31]));
+      }
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
+      if (j == 0) {
+        m = top;
+      } else if (__any_sync(0xffffffffu, top > m + kGrow)) {
+        // O holds the tiles before this one
+        ok = wait_warp(ptx::smem_u32(&sh->odone[g]), (uint32_t)(j - 1) & 1u, abort, a.status);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const float mn = fmaxf(m, top), f = ex2(m - mn);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float v[32];
+          ptx::tmem_ld32(to + 32 * c, v);
+          uint32_t w[2][16];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) w[i >> 4][i & 15] = __float_as_uint(v[i] * f);
+          ptx::tmem_st16(to + 32 * c, w[0]);
+          ptx::tmem_st16(to + 32 * c + 16, w[1]);
+        }
+      }
+      const float2 cc = make_float2(c2, c2), nm = make_float2(-m, -m);
+      float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h == 1) load(1);  // (the first half is still in registers)
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const int e = 2 * i;
+          const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[e >> 5][e & 31]),
+                                                  __uint_as_float(s[e >> 5][(e & 31) + 1])),
+                                      cc, nm);
+          const float2 p = make_float2(ex2(x.x), ex2(x.y));
+          sum[i & 1] = __fadd2_rn(sum[i & 1], p);
+          pk[i & 15] = pack_bf16(p.x, p.y);
+          // P's columns lie over those of S that this thread has read
+          if ((i & 15) == 15) ptx::tmem_st16(ts + 32 * h + (i & 16), pk);
+        }
+      }
+      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh->pfull[g]));
+    }
+    if (ok && ng > 0)
+      ok = wait_warp(ptx::smem_u32(&sh->odone[g]), (uint32_t)(ng - 1) & 1u, abort, a.status);
+    if (ok && ng > 0 && !*abort) {
+      ptx::tc_fence_after();
+      const int64_t r = beg + rr;
+      if (in) a.lse_out[r * a.H + head] = 0.6931471805599453f * m + logf(l);
+      store_row<D / 32>(to, 1.0f / l, (__nv_bfloat16*)a.O + r * a.ldo + (int64_t)head * D, in);
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 1) ptx::tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t forward_as(cudaStream_t st, const AttnArgs& a) {
+  CUtensorMap q, k, v;
+  const int64_t wq = (int64_t)a.H * D, wk = (int64_t)a.Hkv * D;
+  if (!make_map(&q, a.Q, a.T, wq, a.ldq) || !make_map(&k, a.K, a.T, wk, a.ldk) ||
+      !make_map(&v, a.V, a.T, wk, a.ldv))
+    return cudaErrorInvalidValue;
+  auto fn = k_attn_fwd_tc<D>;
+  const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)Cfg<D>::SMEM);
+  if (err != cudaSuccess) return err;
+  const dim3 grid((unsigned)a.H * (unsigned)a.n_seqs,
+                  (unsigned)((a.max_len + 2 * BM - 1) / (2 * BM)));
+  fn<<<grid, THREADS, Cfg<D>::SMEM, st>>>(q, k, v, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_fwd_tc(cudaStream_t st, const AttnArgs& a) {
+  return a.head_dim == 64 ? forward_as<64>(st, a) : forward_as<128>(st, a);
+}
+
+}  // namespace dust
