@@ -162,6 +162,11 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _adr(t: Optional[torch.Tensor]):
+    """A tensor's address as a plain int (the argument types make it a pointer)."""
+    return None if t is None else t.data_ptr()
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return DUST_BF16
@@ -180,7 +185,7 @@ def _matrix(t: torch.Tensor, name: str):
 
 
 def _shape(t: torch.Tensor, shape, name: str):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -249,7 +254,10 @@ def _attn_shapes(X, Q, K_cache, V_cache, E, n_heads):
 def _row_stride(t: torch.Tensor, name: str) -> int:
     """Elements between the rows of a 2-D tensor whose rows are contiguous
     and do not overlap."""
-    rows, width = _matrix(t, name)
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {tuple(shape)}")
+    rows, width = shape
     ld, step = t.stride()
     if (width > 1 and step != 1) or (rows > 1 and ld < width):
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
@@ -368,8 +376,11 @@ class Context:
 
     # -- helpers ---------------------------------------------------------------
     def _bind_stream(self):
-        s = self._stream if self._stream is not None else torch.cuda.current_stream(self.device)
-        self._L.dust_set_stream(self._h, ctypes.c_void_p(s.cuda_stream))
+        if self._stream is not None:
+            s = self._stream.cuda_stream
+        else:
+            s = torch._C._cuda_getCurrentRawStream(self.device)
+        self._L.dust_set_stream(self._h, s)
 
     def _check(self, st: int):
         if st != DUST_OK:
@@ -558,25 +569,25 @@ class Context:
         self._cuda(Z, "Z")
         if tokens is not None:
             self._dev(tokens, "tokens")
-        out = dict(out or {})
-        spec = {}
+        out = dict(out) if out else {}
+        spec = []
         if tokens is not None:
-            spec["logp"] = ((T,), torch.float32)
+            spec.append(("logp", (T,), torch.float32))
         if want_entropy:
-            spec["entropy"] = ((T,), torch.float32)
+            spec.append(("entropy", (T,), torch.float32))
         if top:
-            spec["top_ids"] = ((T, top), torch.int32)
-            spec["top_logp"] = ((T, top), torch.float32)
-        for key, (shape, dt) in spec.items():
+            spec.append(("top_ids", (T, top), torch.int32))
+            spec.append(("top_logp", (T, top), torch.float32))
+        p = dict.fromkeys(("logp", "entropy", "top_ids", "top_logp"))
+        for key, shape, dt in spec:
             if key in out:
                 _check_output(out, key, shape, dt, self.device)
             else:
                 out[key] = self._empty(shape, dt, Z.device)
+            p[key] = out[key].data_ptr()
         self._bind_stream()
-        p = [_ptr(out[key]) if key in spec else None
-             for key in ("logp", "entropy", "top_ids", "top_logp")]
-        self._check(self._L.dust_token_logprobs(self._h, T, V, _dtype_code(Z), _ptr(Z), ld,
-                                                _ptr(tokens), top, *p,
+        self._check(self._L.dust_token_logprobs(self._h, T, V, _dtype_code(Z), Z.data_ptr(), ld,
+                                                _adr(tokens), top, *p.values(),
                                                 FLAG_ASYNC if asynchronous else 0))
         return out
 
@@ -595,24 +606,29 @@ class Context:
         self._dev(teacher_ids, "teacher_ids"), self._dev(teacher_vals, "teacher_vals")
         if weights is not None:
             self._dev(weights, "weights")
-        out = dict(out or {})
+        out = dict(out) if out else {}
         loss = dZ = None
         ldg = V
         if want_loss:
-            _check_output(out, "loss", (T,), torch.float32, self.device)
-            if "loss" not in out:
+            if "loss" in out:
+                _check_output(out, "loss", (T,), torch.float32, self.device)
+            else:
                 out["loss"] = self._empty((T,), torch.float32, Z.device)
             loss = out["loss"]
         if want_grad:
-            _check_output(out, "dZ", (T, V), Z.dtype, self.device, rows=True)
-            if "dZ" not in out:
-                out["dZ"] = self._empty((T, ld), Z.dtype, Z.device)[:, :V]
+            if "dZ" in out:
+                _check_output(out, "dZ", (T, V), Z.dtype, self.device, rows=True)
+                ldg = _row_stride(out["dZ"], "output dZ")
+            else:
+                out["dZ"] = self._empty((T, ld), Z.dtype, Z.device)
+                if ld != V:
+                    out["dZ"] = out["dZ"][:, :V]
+                ldg = ld
             dZ = out["dZ"]
-            ldg = _row_stride(dZ, "output dZ")
         self._bind_stream()
-        self._check(self._L.dust_distill(self._h, T, V, _dtype_code(Z), _ptr(Z), ld,
-                                         _ptr(teacher_ids), _ptr(teacher_vals), k,
-                                         float(temperature), _ptr(weights), _ptr(loss), _ptr(dZ),
+        self._check(self._L.dust_distill(self._h, T, V, _dtype_code(Z), Z.data_ptr(), ld,
+                                         teacher_ids.data_ptr(), teacher_vals.data_ptr(), k,
+                                         float(temperature), _adr(weights), _adr(loss), _adr(dZ),
                                          ldg, FLAG_ASYNC if asynchronous else 0))
         return out
 
@@ -629,18 +645,16 @@ class Context:
                                 max_len, scale)
         for t, n in ((Q, "Q"), (K_cache, "K_cache"), (V_cache, "V_cache")):
             self._cuda(t, n)
-        out = dict(out or {})
-        T = dims.T
-        _check_output(out, "O", tuple(Q.shape), Q.dtype, self.device, rows=True)
-        _check_output(out, "lse", (T, n_heads), torch.float32, self.device)
-        if "O" not in out:
-            out["O"] = self._empty(tuple(Q.shape), Q.dtype, Q.device)
-        if "lse" not in out:
-            out["lse"] = self._empty((T, n_heads), torch.float32, Q.device)
-        dims.ldo = _row_stride(out["O"], "output O")
+        out = dict(out) if out else {}
+        dims.ldo = self._rows_out(out, "O", Q)
+        if "lse" in out:
+            _check_output(out, "lse", (dims.T, n_heads), torch.float32, self.device)
+        else:
+            out["lse"] = self._empty((dims.T, n_heads), torch.float32, Q.device)
         self._attn_call(dims, cu_seqlens, asynchronous)
-        self._check(self._L.dust_attn_forward(self._h, ctypes.byref(dims), _ptr(Q), _ptr(K_cache),
-                                              _ptr(V_cache), _ptr(out["O"]), _ptr(out["lse"])))
+        self._check(self._L.dust_attn_forward(
+            self._h, ctypes.byref(dims), Q.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(),
+            out["O"].data_ptr(), out["lse"].data_ptr()))
         return out
 
     def attn_backward(self, Q, K_cache, V_cache, O, lse, E, *, n_heads, n_kv_heads=None,
@@ -654,7 +668,7 @@ class Context:
         dims = _exact_attn_dims(Q, K_cache, V_cache, n_heads, n_kv_heads, seq_len, cu_seqlens,
                                 max_len, scale)
         for t, n in ((O, "O"), (E, "E")):
-            _shape(t, tuple(Q.shape), n)
+            _shape(t, Q.shape, n)
             if t.dtype != Q.dtype:
                 raise TypeError(f"{n} must have Q's dtype")
         _shape(lse, (dims.T, n_heads), "lse")
@@ -664,19 +678,25 @@ class Context:
             self._cuda(t, n)
         self._dev(lse, "lse")
         dims.ldo, dims.lde = _row_stride(O, "O"), _row_stride(E, "E")
-        out = dict(out or {})
-        for key, like in (("dQ", Q), ("dK", K_cache), ("dV", V_cache)):
-            _check_output(out, key, tuple(like.shape), Q.dtype, self.device, rows=True)
-            if key not in out:
-                out[key] = self._empty(tuple(like.shape), Q.dtype, Q.device)
-        dims.lddq, dims.lddk, dims.lddv = (_row_stride(out[k], f"output {k}")
-                                           for k in ("dQ", "dK", "dV"))
+        out = dict(out) if out else {}
+        dims.lddq = self._rows_out(out, "dQ", Q)
+        dims.lddk = self._rows_out(out, "dK", K_cache)
+        dims.lddv = self._rows_out(out, "dV", V_cache)
         delta = self._empty((dims.T, n_heads), torch.float32, Q.device)
         self._attn_call(dims, cu_seqlens, asynchronous)
         self._check(self._L.dust_attn_backward(
-            self._h, ctypes.byref(dims), _ptr(Q), _ptr(K_cache), _ptr(V_cache), _ptr(O), _ptr(lse),
-            _ptr(E), _ptr(out["dQ"]), _ptr(out["dK"]), _ptr(out["dV"]), _ptr(delta)))
+            self._h, ctypes.byref(dims), Q.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(),
+            O.data_ptr(), lse.data_ptr(), E.data_ptr(), out["dQ"].data_ptr(),
+            out["dK"].data_ptr(), out["dV"].data_ptr(), delta.data_ptr()))
         return out
+
+    def _rows_out(self, out: dict, key: str, like: torch.Tensor) -> int:
+        """The row stride of an output like ``like``, made where it is not given."""
+        if key not in out:
+            out[key] = self._empty(like.shape, like.dtype, like.device)
+            return like.shape[1]
+        _check_output(out, key, like.shape, like.dtype, self.device, rows=True)
+        return _row_stride(out[key], f"output {key}")
 
     def _attn_call(self, dims: DustAttnDims, cu_seqlens, asynchronous: bool):
         if cu_seqlens is not None:

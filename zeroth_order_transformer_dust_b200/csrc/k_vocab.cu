@@ -35,6 +35,9 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float nan_f() { return __int_as_float(0x7fc00000); }
+__device__ __forceinline__ float inf_f() { return __int_as_float(0x7f800000); }
+
 __device__ __forceinline__ float load_f(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float load_f(const __nv_bfloat16* p) {
   return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p)) << 16);
@@ -121,23 +124,32 @@ __device__ __forceinline__ void stat_rescale(Stat& a, float m, float k2) {
   a.m = m;
 }
 
+// N (even) more elements, two per packed operation; returns their maximum.
 template <bool ENT, int N>
-__device__ __forceinline__ void stat_add(Stat& a, const float (&z)[N], float k2) {
+__device__ __forceinline__ float stat_add(Stat& a, const float (&z)[N], float k2) {
   float cm = z[0];
 #pragma unroll
   for (int i = 1; i < N; ++i) cm = fmaxf(cm, z[i]);
   if (cm > a.m) stat_rescale<ENT>(a, cm, k2);
-  float s[2] = {0.0f, 0.0f}, u[2] = {0.0f, 0.0f};
+  const float2 nm = make_float2(-a.m, -a.m), kk = make_float2(k2, k2);
+  float2 s = make_float2(0.0f, 0.0f), u = make_float2(0.0f, 0.0f);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float d = z[i] - a.m;
-    const float e = ex2(d * k2);
-    s[i & 1] += e;
+  for (int i = 0; i < N; i += 2) {
+    const float2 d = __fadd2_rn(make_float2(z[i], z[i + 1]), nm);
+    const float2 x = __fmul2_rn(d, kk);
+    const float2 e = make_float2(ex2(x.x), ex2(x.y));
+    s = __fadd2_rn(s, e);
     // exp(-1e4) = 0: the clamp only keeps 0 x (-inf) out
-    if (ENT) u[i & 1] = fmaf(fmaxf(d, -1e4f), e, u[i & 1]);
+    if (ENT) u = __ffma2_rn(make_float2(fmaxf(d.x, -1e4f), fmaxf(d.y, -1e4f)), e, u);
   }
-  a.s += s[0] + s[1];
-  if (ENT) a.u += u[0] + u[1];
+  a.s += s.x + s.y;
+  if (ENT) a.u += u.x + u.y;
+  return cm;
+}
+template <bool ENT>
+__device__ __forceinline__ void stat_add1(Stat& a, float z, float k2) {
+  const float pair[2] = {z, -inf_f()};
+  stat_add<ENT, 2>(a, pair, k2);
 }
 
 template <bool ENT>
@@ -203,9 +215,6 @@ __device__ __forceinline__ Stat stat_cluster(const Stat& a, float k2, Stat* mine
   return t;
 }
 
-__device__ __forceinline__ float nan_f() { return __int_as_float(0x7fc00000); }
-__device__ __forceinline__ float inf_f() { return __int_as_float(0x7f800000); }
-
 // ---- log probabilities, entropy, top alternatives -----------------------------------
 //
 // Bound by reading the logits once. Without alternatives a thread streams
@@ -222,9 +231,9 @@ constexpr int kLpThreads = 256;
 constexpr int kTopTile = 8;                           // elements per thread and tile
 constexpr int kTopTileElems = kLpThreads * kTopTile;  // a tile
 constexpr int kTopList = 4096;                        // list entries, a power of two
-constexpr int kTopCut = 512;                          // the list is cut when it grows past this
+constexpr int kTopCut = 256;                          // the list is cut at 2 n entries, at most here
 static_assert(kTopCut + 16 + kTopTileElems <= kTopList, "a tile must fit the list");
-static_assert(kTopLimit <= kLpThreads && kTopLimit < kTopCut, "one output entry per thread");
+static_assert(2 * kTopLimit <= kTopCut && kTopCut <= kLpThreads, "one entry per thread");
 static_assert(kMaxCluster * kTopLimit <= kTopList, "the CTAs' lists meet in one");
 
 __device__ __forceinline__ uint32_t order_bits(float z) {
@@ -234,8 +243,8 @@ __device__ __forceinline__ uint32_t order_bits(float z) {
 __device__ __forceinline__ float order_value(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
-__device__ __forceinline__ uint64_t top_key(float z, int64_t col) {
-  return ((uint64_t)order_bits(z) << 32) | (uint32_t)(0xffffffffu - (uint32_t)col);
+__device__ __forceinline__ uint64_t top_key(float z, uint32_t col) {
+  return ((uint64_t)order_bits(z) << 32) | (0xffffffffu - col);
 }
 // The smallest float above z: z' >= next_up(z) exactly when z' > z.
 __device__ __forceinline__ float next_up(float z) {
@@ -264,9 +273,38 @@ __device__ void sort_list(uint64_t* list, int count) {
   }
 }
 
+// The same for a list of at most an entry per thread: every entry counts the
+// keys above it (all keys differ) and moves to its rank, in three barriers
+// instead of the sort's thirty.
+__device__ void rank_list(uint64_t* list, int count) {
+  const int tid = threadIdx.x;
+  if (tid == 0) list[count] = 0;  // (below every key)
+  __syncthreads();
+  uint64_t key = 0;
+  int rank = 0;
+  if (tid < count) {
+    key = list[tid];
+#pragma unroll 4
+    for (int i = 0; i < count; i += 2) {
+      const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(list + i);
+      rank += (k.x > key) + (k.y > key);
+    }
+  }
+  __syncthreads();
+  if (tid < count) list[rank] = key;
+  __syncthreads();
+}
+__device__ __forceinline__ void order_list(uint64_t* list, int count) {
+  if (count <= kLpThreads)
+    rank_list(list, count);
+  else
+    sort_list(list, count);
+}
+
 struct TopState {
   int count;
-  float thr;  // elements >= thr enter
+  float thr;       // elements >= thr enter
+  uint32_t first;  // order_bits of the first threshold
 };
 
 struct LogprobArgs {
@@ -281,19 +319,38 @@ struct LogprobArgs {
 };
 
 template <typename E, bool TOP>
-__global__ __launch_bounds__(kLpThreads) void k_token_logprobs(const E* __restrict__ Z,
-                                                               LogprobArgs a, int ranks) {
+__global__ __launch_bounds__(kLpThreads, 4) void k_token_logprobs(
+    const E* __restrict__ Z, LogprobArgs a, int ranks) {
   constexpr int N = Vec<E>::N;
-  constexpr int U = TOP ? kTopTile / N : 16 / N;  // vectors per thread and tile
-  extern __shared__ uint64_t list[];              // TOP
+  // vectors per thread and tile, and tiles whose loads are in flight: 64 to 128
+  // bytes per thread, about 100 KB an SM, cover the latency of HBM
+  constexpr int W = TOP ? kTopTile : 16;  // elements per thread and tile
+  constexpr int U = W / N, TILE = U * kLpThreads;
+  constexpr int AHEAD = TOP ? (sizeof(E) == 4 ? 3 : 4) : (sizeof(E) == 4 ? 2 : 3);
+  extern __shared__ __align__(16) uint64_t list[];  // TOP
   __shared__ Stat sh_warp[kLpThreads / 32], sh_cta;
   __shared__ TopState top;
+  __shared__ __align__(16) float sh_max[TOP ? kLpThreads : 4];
   const int tid = threadIdx.x;
   const int rank = ranks > 1 ? (int)ptx::cluster_ctarank() : 0;
   const int64_t t = blockIdx.x / ranks;
   const E* row = Z + t * a.ld;
   const Slice sl = slice_of(row, a.V, rank, ranks);
-  const uint4* body = reinterpret_cast<const uint4*>(row + sl.head);
+  const int nv = (int)(sl.v1 - sl.v0);  // (V < 2^31)
+  const uint4* src = reinterpret_cast<const uint4*>(row + sl.head) + sl.v0 + tid;
+  uint4 w[AHEAD][U];
+  auto fetch = [&](uint4 (&x)[U], int v) {
+    if (v + TILE <= nv) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) x[i] = __ldcs(src + v + i * kLpThreads);
+    } else if (v < nv) {
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (v + i * kLpThreads + tid < nv) x[i] = __ldcs(src + v + i * kLpThreads);
+    }
+  };
+#pragma unroll
+  for (int q = 0; q < AHEAD; ++q) fetch(w[q], q * TILE);
   Stat st = stat_none();
   bool grown = false;
   if (TOP) {
@@ -303,93 +360,91 @@ __global__ __launch_bounds__(kLpThreads) void k_token_logprobs(const E* __restri
     }
     __syncthreads();
   }
-  auto enter = [&](float z, int64_t col) {
+  const int cut_at = min(max(2 * a.n, 96), kTopCut);
+  auto enter = [&](float z, uint32_t col) {
     const int slot = atomicAdd(&top.count, 1);
     list[slot] = top_key(z, col);
-    grown |= slot >= kTopCut;
+    grown |= slot >= cut_at;
   };
   auto edge = [&](int64_t col) {
     const float z = load_f(row + col);
-    const float one[1] = {z};
-    stat_add<true, 1>(st, one, kLog2e);
-    if (TOP && z >= top.thr) enter(z, col);
+    stat_add1<true>(st, z, kLog2e);
+    if (TOP && z >= top.thr) enter(z, (uint32_t)col);
   };
   if (rank == 0 && tid < sl.head) edge(tid);
-  // sort, cut to the n best and move the threshold past the n-th: every later
+  // order, cut to the n best and move the threshold past the n-th: every later
   // element has a higher index, so among equal values it loses
   auto cut = [&]() {
     const int count = top.count;
-    sort_list(list, count);
-    if (tid == 0) {
-      if (count >= a.n) {
-        top.count = a.n;
-        top.thr = next_up(order_value((uint32_t)(list[a.n - 1] >> 32)));
-      }
+    order_list(list, count);
+    if (tid == 0) {  // (cut_at < count, n <= cut_at / 2 or n = 128)
+      top.count = min(count, a.n);
+      if (count >= a.n) top.thr = next_up(order_value((uint32_t)(list[a.n - 1] >> 32)));
     }
     grown = false;
     __syncthreads();
   };
-
-  uint4 w[U];
-  auto fetch = [&](int64_t v) {
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int64_t k = v + (int64_t)i * kLpThreads + tid;
-      if (k < sl.v1) w[i] = __ldcs(body + k);
+  // the first threshold, the n-th largest of the threads' maxima over the first
+  // tile: the largest maximum that n maxima are not below
+  auto first_threshold = [&](float mx) {
+    sh_max[tid] = mx;
+    if (tid == 0) top.first = 0;
+    __syncthreads();
+    int ge = 0;
+#pragma unroll 4
+    for (int i = 0; i < kLpThreads; i += 4) {
+      const float4 o = *reinterpret_cast<const float4*>(sh_max + i);
+      ge += (o.x >= mx) + (o.y >= mx) + (o.z >= mx) + (o.w >= mx);
     }
+    const uint32_t best = __reduce_max_sync(0xffffffffu, ge >= a.n ? order_bits(mx) : 0u);
+    if ((tid & 31) == 0) atomicMax(&top.first, best);
+    __syncthreads();
+    if (tid == 0) top.thr = fmaxf(order_value(top.first), -FLT_MAX);
+    __syncthreads();
   };
-  fetch(sl.v0);
-  for (int64_t v = sl.v0; v < sl.v1; v += (int64_t)U * kLpThreads) {
-    float z[U][N];
-    float cm[U];
+
+  const uint32_t col0 = (uint32_t)(sl.head + (sl.v0 + tid) * N);
+  for (int v0 = 0; v0 < nv; v0 += AHEAD * TILE) {
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int64_t k = v + (int64_t)i * kLpThreads + tid;
-      if (k < sl.v1) {
-        unpack(w[i], z[i]);
-      } else {
-#pragma unroll
-        for (int q = 0; q < N; ++q) z[i][q] = -inf_f();
-      }
-    }
-    fetch(v + (int64_t)U * kLpThreads);  // the next tile's loads run under this tile's math
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      stat_add<true, N>(st, z[i], kLog2e);
-      if (TOP) {
-        cm[i] = z[i][0];
-#pragma unroll
-        for (int q = 1; q < N; ++q) cm[i] = fmaxf(cm[i], z[i][q]);
-      }
-    }
-    if (TOP) {
-      if (v == sl.v0) {
-        // the first threshold: the head elements already listed stay
-        float mx = cm[0];
-#pragma unroll
-        for (int i = 1; i < U; ++i) mx = fmaxf(mx, cm[i]);
-        __syncthreads();
-        uint64_t* scratch = list + 2048;  // apart from the head's entries
-        scratch[tid] = (uint64_t)order_bits(mx) << 32 | (uint32_t)tid;
-        __syncthreads();
-        sort_list(scratch, kLpThreads);
-        if (tid == 0) {
-          const float b = order_value((uint32_t)(scratch[a.n - 1] >> 32));
-          top.thr = fmaxf(b, -FLT_MAX);
-        }
-        __syncthreads();
-      }
-      const float thr = top.thr;
+    for (int q = 0; q < AHEAD; ++q) {
+      const int v = v0 + q * TILE;
+      if (v >= nv) break;
+      float z[W];
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        if (cm[i] >= thr) {
-          const int64_t col = sl.head + (v + (int64_t)i * kLpThreads + tid) * N;
+        float x[N];
+        unpack(w[q][i], x);
 #pragma unroll
-          for (int q = 0; q < N; ++q)
-            if (z[i][q] >= thr) enter(z[i][q], col + q);
-        }
+        for (int e = 0; e < N; ++e) z[i * N + e] = x[e];
       }
-      if (__syncthreads_or(grown)) cut();
+      if (v + TILE > nv) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (v + i * kLpThreads + tid >= nv) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) z[i * N + e] = -inf_f();
+          }
+      }
+      fetch(w[q], v + AHEAD * TILE);
+      const float mx = stat_add<true, W>(st, z, kLog2e);
+      if (TOP) {
+        if (v == 0) first_threshold(isnan(mx) ? -inf_f() : mx);
+        const float thr = top.thr;
+        if (mx >= thr) {
+          uint32_t in = 0;
+#pragma unroll
+          for (int e = 0; e < W; ++e) in |= z[e] >= thr ? 1u << e : 0u;
+          do {
+            const int e = __ffs((int)in) - 1;
+            in &= in - 1;
+            float x = z[0];
+#pragma unroll
+            for (int k = 1; k < W; ++k) x = e == k ? z[k] : x;
+            enter(x, col0 + (uint32_t)((v + e / N * kLpThreads) * N + e % N));
+          } while (in);
+        }
+        if (__syncthreads_or(grown)) cut();
+      }
     }
   }
   if (sl.tail0 + tid < sl.tail1) edge(sl.tail0 + tid);
@@ -397,7 +452,7 @@ __global__ __launch_bounds__(kLpThreads) void k_token_logprobs(const E* __restri
   st = stat_block<true>(st, kLog2e, sh_warp);
   if (TOP) {  // (the barrier inside stat_block ordered the last entries)
     const int count = top.count;
-    sort_list(list, count);
+    order_list(list, count);
     if (tid == 0) top.count = min(count, a.n);
     __syncthreads();
   }
@@ -413,7 +468,7 @@ __global__ __launch_bounds__(kLpThreads) void k_token_logprobs(const E* __restri
       total += cnt;
     }
     __syncthreads();
-    sort_list(list, total);
+    order_list(list, total);
     if (tid == 0) top.count = min(total, a.n);
     __syncthreads();
   }
@@ -583,8 +638,7 @@ __global__ __launch_bounds__(kDsThreads, 2) void k_distill(const E* Z, E* dZ, Di
   // statistics of the row
   Stat st = stat_none();
   auto edge = [&](int64_t col) {
-    const float one[1] = {load_rw(row + col)};
-    stat_add<false, 1>(st, one, a.k2);
+    stat_add1<false>(st, load_rw(row + col), a.k2);
   };
   if (rank == 0 && tid < sl.head) edge(tid);
   if (sl.tail0 + tid < sl.tail1) edge(sl.tail0 + tid);
