@@ -223,7 +223,7 @@ __device__ __forceinline__ Stat stat_cluster(const Stat& a, float k2, Stat* mine
 // enters when it is not below the CTA's threshold, and when the list has grown
 // past its limit it is sorted, cut to n, and the threshold moves to the n-th.
 // The first threshold is the n-th largest of the threads' maxima over the
-// first tile (n elements at least are not below it), so on ordinary rows about
+// first tiles (n elements at least are not below it), so on ordinary rows about
 // n (1 + ln(V / tile)) elements ever enter. Any row is handled: a tile that
 // enters whole fits the list. List order depends on timing, the sorted list
 // does not: keys are (value, ~index), all different.
@@ -234,7 +234,7 @@ constexpr int kTopList = 4096;                        // list entries, a power o
 constexpr int kTopCut = 256;                          // the list is cut at 2 n entries, at most here
 static_assert(kTopCut + 16 + kTopTileElems <= kTopList, "a tile must fit the list");
 static_assert(2 * kTopLimit <= kTopCut && kTopCut <= kLpThreads, "one entry per thread");
-static_assert(kMaxCluster * kTopLimit <= kTopList, "the CTAs' lists meet in one");
+static_assert(kMaxCluster <= kLpThreads / 32 && kMaxCluster * kTopLimit <= kTopList, "the CTAs' lists meet in one");
 
 __device__ __forceinline__ uint32_t order_bits(float z) {
   const uint32_t b = __float_as_uint(z + 0.0f);  // -0 counts as +0
@@ -384,8 +384,8 @@ __global__ __launch_bounds__(kLpThreads, 4) void k_token_logprobs(
     grown = false;
     __syncthreads();
   };
-  // the first threshold, the n-th largest of the threads' maxima over the first
-  // tile: the largest maximum that n maxima are not below
+  // the first threshold, the n-th largest of the threads' maxima over the tiles
+  // in flight: the largest maximum that n maxima are not below
   auto first_threshold = [&](float mx) {
     sh_max[tid] = mx;
     if (tid == 0) top.first = 0;
@@ -404,6 +404,20 @@ __global__ __launch_bounds__(kLpThreads, 4) void k_token_logprobs(
   };
 
   const uint32_t col0 = (uint32_t)(sl.head + (sl.v0 + tid) * N);
+  if (TOP) {
+    float mx = -inf_f();
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q)
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (q * TILE + i * kLpThreads + tid < nv) {
+          float x[N];
+          unpack(w[q][i], x);
+#pragma unroll
+          for (int e = 0; e < N; ++e) mx = fmaxf(mx, x[e]);  // (NaN is passed over)
+        }
+    first_threshold(mx);
+  }
   for (int v0 = 0; v0 < nv; v0 += AHEAD * TILE) {
 #pragma unroll
     for (int q = 0; q < AHEAD; ++q) {
@@ -428,7 +442,6 @@ __global__ __launch_bounds__(kLpThreads, 4) void k_token_logprobs(
       fetch(w[q], v + AHEAD * TILE);
       const float mx = stat_add<true, W>(st, z, kLog2e);
       if (TOP) {
-        if (v == 0) first_threshold(isnan(mx) ? -inf_f() : mx);
         const float thr = top.thr;
         if (mx >= thr) {
           uint32_t in = 0;
@@ -452,20 +465,28 @@ __global__ __launch_bounds__(kLpThreads, 4) void k_token_logprobs(
   st = stat_block<true>(st, kLog2e, sh_warp);
   if (TOP) {  // (the barrier inside stat_block ordered the last entries)
     const int count = top.count;
-    order_list(list, count);
+    if (ranks == 1 || count > a.n) order_list(list, count);
     if (tid == 0) top.count = min(count, a.n);
     __syncthreads();
   }
   const Stat all = stat_cluster<true>(st, kLog2e, &sh_cta, ranks);
   if (TOP && ranks > 1 && rank == 0) {
-    // the CTAs' sorted lists behind one another, then one sort
-    int total = top.count;
-    for (int r = 1; r < ranks; ++r) {
-      const int cnt = __float_as_int(
-          ld_cluster_f32(ptx::mapa_shared(ptx::smem_u32(&top.count), (uint32_t)r)));
+    // the CTAs' best behind one another, a warp for each, then in order
+    const int r = tid >> 5, lane = tid & 31;
+    int cnt = 0, at = 0, total = 0;
+    if (lane < ranks)
+      cnt = __float_as_int(
+          ld_cluster_f32(ptx::mapa_shared(ptx::smem_u32(&top.count), (uint32_t)lane)));
+    for (int q = 0; q < ranks; ++q) {
+      const int c = __shfl_sync(0xffffffffu, cnt, q);
+      at += q < r ? c : 0;
+      total += c;
+    }
+    const int mine = __shfl_sync(0xffffffffu, cnt, r);
+    __syncthreads();
+    if (r > 0 && r < ranks) {
       const uint32_t src = ptx::mapa_shared(ptx::smem_u32(list), (uint32_t)r);
-      for (int i = tid; i < cnt; i += kLpThreads) list[total + i] = ld_cluster_u64(src + 8u * i);
-      total += cnt;
+      for (int i = lane; i < mine; i += 32) list[at + i] = ld_cluster_u64(src + 8u * i);
     }
     __syncthreads();
     order_list(list, total);
