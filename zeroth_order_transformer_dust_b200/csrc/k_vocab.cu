@@ -18,6 +18,7 @@
 // Few rows do not fill the GPU with one CTA each, so a row may be split over a
 // cluster of up to 8 CTAs whose triples (and top lists) meet in distributed
 // shared memory: still one launch.
+#include <atomic>
 #include <cfloat>
 
 #include "internal.cuh"
@@ -86,23 +87,22 @@ __device__ __forceinline__ uint4 pack(const float (&v)[8]) {
 }
 
 // A CTA's part of a row: `head` elements up to the first 16-byte boundary (rank
-// 0's), whole vectors [v0, v1) of the aligned body, and the `tail` after it
-// (the last rank's). body = head, in elements from the row's start.
+// 0's), whole vectors [v0, v1) of the aligned body behind them, and the `tail`
+// elements [tail0, tail1) after it (the last rank's). (V < 2^31.)
 struct Slice {
-  int64_t head, v0, v1, tail0, tail1;
+  int head, v0, v1, tail0, tail1;
 };
 template <typename E>
 __device__ __forceinline__ Slice slice_of(const E* row, int64_t V, int rank, int ranks) {
   constexpr int N = Vec<E>::N;
   Slice s;
-  int64_t head = (int64_t)(((16 - ((uintptr_t)row & 15)) & 15) / sizeof(E));
-  if (head > V) head = V;
-  const int64_t nv = (V - head) / N;
-  s.head = head;
-  s.v0 = nv * rank / ranks;
-  s.v1 = nv * (rank + 1) / ranks;
-  s.tail0 = head + nv * N;
-  s.tail1 = rank == ranks - 1 ? V : s.tail0;
+  const int head = (int)((16 - ((uintptr_t)row & 15)) & 15) / (int)sizeof(E);
+  s.head = head < V ? head : (int)V;
+  const int nv = ((int)V - s.head) / N;
+  s.v0 = (int)((int64_t)nv * rank / ranks);
+  s.v1 = (int)((int64_t)nv * (rank + 1) / ranks);
+  s.tail0 = s.head + nv * N;
+  s.tail1 = rank == ranks - 1 ? (int)V : s.tail0;
   return s;
 }
 
@@ -152,35 +152,48 @@ __device__ __forceinline__ void stat_add1(Stat& a, float z, float k2) {
   stat_add<ENT, 2>(a, pair, k2);
 }
 
+// A warp's statistics, the same value in every lane: the maximum first, so
+// that each lane rescales once; the butterflies add in a fixed order.
 template <bool ENT>
-__device__ __forceinline__ Stat stat_join(Stat a, const Stat& b, float k2) {
-  const float m = fmaxf(a.m, b.m);
-  Stat c = b;
+__device__ __forceinline__ Stat stat_warp(Stat a, float k2) {
+  float m = a.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   stat_rescale<ENT>(a, m, k2);
-  stat_rescale<ENT>(c, m, k2);
-  a.s += c.s;
-  if (ENT) a.u += c.u;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+    if (ENT) a.u += __shfl_xor_sync(0xffffffffu, a.u, o);
+  }
   return a;
 }
 
-// The CTA's statistics, the same value in every thread: butterflies inside the
-// warps (every lane combines the same pairs), then the warps in order.
+// Barrier of the first `threads` threads of a CTA (all but a producer warp), and
+// the same with the or of a flag.
+__device__ __forceinline__ void sync_threads(int threads) {
+  asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+}
+__device__ __forceinline__ bool sync_threads_or(bool flag, int threads) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.or.pred p, 1, %2, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)flag), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+
+// The statistics of the first `threads` threads, the same value in each.
 template <bool ENT>
-__device__ __forceinline__ Stat stat_block(Stat a, float k2, Stat* sh) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Stat b = stat_none();
-    b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
-    b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
-    if (ENT) b.u = __shfl_xor_sync(0xffffffffu, a.u, o);
-    a = stat_join<ENT>(a, b, k2);
-  }
+__device__ __forceinline__ Stat stat_block(Stat a, float k2, Stat* sh, int threads) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  a = stat_warp<ENT>(a, k2);
   if (lane == 0) sh[warp] = a;
-  __syncthreads();
-  Stat t = sh[0];
-  for (int w = 1; w < warps; ++w) t = stat_join<ENT>(t, sh[w], k2);
-  return t;
+  sync_threads(threads);
+  return stat_warp<ENT>(lane < threads / 32 ? sh[lane] : stat_none(), k2);
 }
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
@@ -202,17 +215,15 @@ __device__ __forceinline__ Stat stat_cluster(const Stat& a, float k2, Stat* mine
   if (ranks == 1) return a;
   if (threadIdx.x == 0) *mine = a;
   ptx::cluster_sync();
-  const uint32_t here = ptx::smem_u32(mine);
+  const int lane = threadIdx.x & 31;
   Stat t = stat_none();
-  for (int r = 0; r < ranks; ++r) {
-    const uint32_t p = ptx::mapa_shared(here, (uint32_t)r);
-    Stat b = stat_none();
-    b.m = ld_cluster_f32(p);
-    b.s = ld_cluster_f32(p + 4);
-    if (ENT) b.u = ld_cluster_f32(p + 8);
-    t = r == 0 ? b : stat_join<ENT>(t, b, k2);
+  if (lane < ranks) {
+    const uint32_t p = ptx::mapa_shared(ptx::smem_u32(mine), (uint32_t)lane);
+    t.m = ld_cluster_f32(p);
+    t.s = ld_cluster_f32(p + 4);
+    if (ENT) t.u = ld_cluster_f32(p + 8);
   }
-  return t;
+  return stat_warp<ENT>(t, k2);
 }
 
 // ---- log probabilities, entropy, top alternatives -----------------------------------
@@ -319,7 +330,7 @@ struct LogprobArgs {
 };
 
 template <typename E, bool TOP>
-__global__ __launch_bounds__(kLpThreads, 4) void k_token_logprobs(
+__global__ __launch_bounds__(kLpThreads, TOP ? 4 : 3) void k_token_logprobs(
     const E* __restrict__ Z, LogprobArgs a, int ranks) {
   constexpr int N = Vec<E>::N;
   // vectors per thread and tile, and tiles whose loads are in flight: 64 to 128
@@ -336,7 +347,7 @@ __global__ __launch_bounds__(kLpThreads, 4) void k_token_logprobs(
   const int64_t t = blockIdx.x / ranks;
   const E* row = Z + t * a.ld;
   const Slice sl = slice_of(row, a.V, rank, ranks);
-  const int nv = (int)(sl.v1 - sl.v0);  // (V < 2^31)
+  const int nv = sl.v1 - sl.v0;
   const uint4* src = reinterpret_cast<const uint4*>(row + sl.head) + sl.v0 + tid;
   uint4 w[AHEAD][U];
   auto fetch = [&](uint4 (&x)[U], int v) {
@@ -462,7 +473,7 @@ __global__ __launch_bounds__(kLpThreads, 4) void k_token_logprobs(
   }
   if (sl.tail0 + tid < sl.tail1) edge(sl.tail0 + tid);
 
-  st = stat_block<true>(st, kLog2e, sh_warp);
+  st = stat_block<true>(st, kLog2e, sh_warp, kLpThreads);
   if (TOP) {  // (the barrier inside stat_block ordered the last entries)
     const int count = top.count;
     if (ranks == 1 || count > a.n) order_list(list, count);
@@ -526,21 +537,25 @@ __global__ __launch_bounds__(kLpThreads, 4) void k_token_logprobs(
 // ---- distillation from a teacher's top logits ---------------------------------------
 //
 // The gradient reads and writes every logit once, which is its bound: 2 V
-// elements a row. A CTA copies its part of the row into shared memory by bulk
-// copies, takes the statistics from the chunks as they land, and forms the
-// gradient from shared memory, so HBM is read once whatever L2 holds. Two CTAs
-// share an SM: one writes while the other's copies are in flight. A row longer
-// than a CTA's buffer is split over a cluster; past 8 buffers (kReread) the
-// second pass reads the row from global memory again.
+// elements a row. A CTA (or a cluster, for rows longer than a CTA's buffer) works
+// through rows of its own: it copies its part of a row into shared memory by
+// bulk copies, takes the statistics from the chunks as they land, and forms the
+// gradient from shared memory, so HBM is read once whatever L2 holds. As soon as
+// a chunk's gradient is written the same chunk of the next row is copied in, so
+// reads and writes overlap within the CTA; two CTAs share an SM. Rows past 8
+// buffers (kReread) are read from global memory twice. The loss alone is a
+// streaming pass. The copies are a warp's own (warp 15): refilled by one of the
+// computing threads, who then waits for the others chunk by chunk, the same
+// scheme took 583 us where this one takes @@ (8192 x 50304 bf16).
 enum DistillMode { kLossOnly = 0, kResident = 1, kReread = 2 };
-constexpr int kDsThreads = 512;
+constexpr int kDsThreads = 480;             // (loss alone: kLpThreads, for more rows at a time)
 constexpr int kMaxTeacher = kTopLimit;
-constexpr int kChunk = 8192;                // bytes of one bulk copy
-constexpr int kBufBytes = 13 * kChunk;      // 104 KB: two CTAs fit an SM's shared memory
+constexpr int kChunk = kDsThreads * 32;     // bytes of one bulk copy: two vectors per thread
+constexpr int kBufBytes = 7 * kChunk;       // 105 KB: two CTAs fit an SM's shared memory
 constexpr int kMaxChunks = kBufBytes / kChunk;
 
 struct DistillArgs {
-  int64_t ld, ldg, V;
+  int64_t T, ld, ldg, V;
   const int32_t* ids;    // T x k
   const float* vals;     // T x k
   int k;
@@ -551,215 +566,322 @@ struct DistillArgs {
 };
 
 struct DistillShared {
-  Stat warp[kDsThreads / 32], cta;
-  float q[kMaxTeacher], z[kMaxTeacher], red[4];
-  int32_t id[kMaxTeacher];
-  uint64_t bar[kMaxChunks];
+  Stat warp[kDsThreads / 32], cta[2];
+  int4 id[kMaxTeacher / 4];    // the row's entries, -1: none
+  float4 q[kMaxTeacher / 4];   // their weights, up to the sum
+  float red[2][4], loss[4], scale;
+  uint64_t full[kMaxChunks], empty[kMaxChunks];
 };
 
 constexpr uint64_t kCopyWaitNs = 2000000000ull;  // 2 s
 
-// Wait for a chunk's copy, for at most kCopyWaitNs: past that the call reports
-// a timeout and its outputs are unspecified. Every chunk is waited for, so no
-// copy is in flight when the CTA leaves.
-__device__ __noinline__ void wait_copy(uint32_t bar, uint32_t* status) {
+// Wait for a phase of a barrier, for at most kCopyWaitNs: past that the call
+// reports a timeout and its outputs are unspecified. Every copy is waited for,
+// so none is in flight when the CTA leaves.
+__device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, uint32_t* status) {
   const uint64_t t0 = ptx::globaltimer_ns();
-  while (!ptx::mbar_try_wait(bar, 0)) {
+  while (!ptx::mbar_try_wait(bar, parity)) {
     if (ptx::globaltimer_ns() - t0 > kCopyWaitNs) {
       atomicOr(status, kStatusTimeout);
       return;
     }
   }
 }
+__device__ __forceinline__ void wait_phase(uint64_t& bar, uint32_t parity, uint32_t* status) {
+  const uint32_t b = ptx::smem_u32(&bar);
+  if (!ptx::mbar_try_wait(b, parity)) wait_slow(b, parity, status);
+}
 
 template <typename E, int MODE>
-__global__ __launch_bounds__(kDsThreads, 2) void k_distill(const E* Z, E* dZ, DistillArgs a,
-                                                        int ranks) {
+__global__ __launch_bounds__(MODE == kLossOnly ? kLpThreads
+                                               : kDsThreads + (MODE == kResident ? 32 : 0),
+                             MODE == kResident ? 2 : (MODE == kLossOnly ? 4 : 1)) void k_distill(const E* Z, E* dZ,
+                                                                       DistillArgs a, int ranks) {
   constexpr int N = Vec<E>::N;
+  constexpr int THREADS = MODE == kLossOnly ? kLpThreads : kDsThreads;
   extern __shared__ __align__(128) uint8_t buf[];  // kResident: the slice's vectors
   __shared__ DistillShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = ranks > 1 ? (int)ptx::cluster_ctarank() : 0;
-  const int64_t t = blockIdx.x / ranks;
-  const E* row = Z + t * a.ld;
-  E* out = MODE == kLossOnly ? nullptr : dZ + t * a.ldg;
-  const Slice sl = slice_of(row, a.V, rank, ranks);
-  const uint4* body = reinterpret_cast<const uint4*>(row + sl.head);
-  const float weight = a.weights ? a.weights[t] : 1.0f;
-
-  // the teacher's distribution over its kept set, by the first warps: one
-  // entry per thread, absent where its id is -1 or its value -inf
+  const int64_t step = gridDim.x / ranks;
+  // this thread's teacher entry of a row: absent (-1) where its id is -1 or its
+  // value -inf
   int32_t id = -1;
-  float v = -inf_f();
-  if (tid < a.k) {
-    id = a.ids[t * a.k + tid];
-    if (id != -1) {
-      if (id < 0 || (int64_t)id >= a.V) {
+  float v = -inf_f(), weight = 1.0f;
+  auto entry = [&](int64_t t) {  // as stored
+    id = -1;
+    if (t >= a.T) return;
+    weight = a.weights ? a.weights[t] : 1.0f;
+    if (tid < a.k) {
+      id = a.ids[t * a.k + tid];
+      v = a.vals[t * a.k + tid];
+    }
+  };
+  // From row t on, whose entry is loaded, the first that is not left out (T:
+  // none). A row without a teacher entry, or of weight 0, gets zeros and its
+  // logits are not read. All CTAs of a cluster see the same rows.
+  auto next_live = [&](int64_t t) {
+    for (; t < a.T; t += step, entry(t)) {
+      if (id != -1 && (id < 0 || (int64_t)id >= a.V)) {
         atomicOr(a.status, kStatusBadTarget);
         id = -1;
-      } else {
-        v = a.vals[t * a.k + tid];
-        if (v == -inf_f()) id = -1;
       }
+      if (id == -1 || v == -inf_f()) {
+        id = -1;
+        v = -inf_f();
+      }
+      if (sync_threads_or(id >= 0, THREADS) && weight != 0.0f) return t;
+      if (MODE != kLossOnly) {
+        const Slice sl = slice_of(Z + t * a.ld, a.V, rank, ranks);
+        E* out = dZ + t * a.ldg;
+        const int c0 = rank == 0 ? 0 : sl.head + sl.v0 * N;
+        const int c1 = rank == ranks - 1 ? (int)a.V : sl.head + sl.v1 * N;
+        const int lead = (int)((16 - ((uintptr_t)(out + c0) & 15)) & 15) / (int)sizeof(E);
+        const int c = min(c0 + lead, c1), n = (c1 - c) / N;
+        if (c0 + tid < c) store_e(out + c0 + tid, 0.0f);
+        for (int i = tid; i < n; i += THREADS)
+          __stcs(reinterpret_cast<uint4*>(out + c) + i, make_uint4(0, 0, 0, 0));
+        if (c + n * N + tid < c1) store_e(out + c + n * N + tid, 0.0f);
+      }
+      if (rank == 0 && tid == 0 && a.loss) a.loss[t] = 0.0f;
     }
-    sh.id[tid] = id;
-  }
-  // a row without a teacher entry, or of weight 0, is left out: its logits are not read
-  const bool live = __syncthreads_or(id >= 0) && weight != 0.0f;
-  // the slice's columns of the gradient, [c0, c1)
-  const int64_t c0 = rank == 0 ? 0 : sl.head + sl.v0 * N;
-  const int64_t c1 = rank == ranks - 1 ? a.V : sl.head + sl.v1 * N;
-  if (!live) {
-    if (MODE != kLossOnly)
-      for (int64_t c = c0 + tid; c < c1; c += kDsThreads) store_e(out + c, 0.0f);
-    if (rank == 0 && tid == 0 && a.loss) a.loss[t] = 0.0f;
-    return;  // every CTA of the cluster leaves here together
-  }
-  const int nbytes = (int)((sl.v1 - sl.v0) * 16);
-  const int chunks = MODE == kResident ? (nbytes + kChunk - 1) / kChunk : 0;
-  if (MODE == kResident && tid == 0) {
-    for (int c = 0; c < chunks; ++c) ptx::mbar_init(ptx::smem_u32(&sh.bar[c]), 1);
-    ptx::fence_barrier_init();
-    ptx::fence_proxy_async();
-    for (int c = 0; c < chunks; ++c) {
-      const uint32_t n = (uint32_t)min(kChunk, nbytes - c * kChunk);
-      const uint32_t bar = ptx::smem_u32(&sh.bar[c]);
-      ptx::mbar_expect_tx(bar, n);
-      ptx::bulk_load(ptx::smem_u32(buf) + c * kChunk,
-                     reinterpret_cast<const uint8_t*>(body + sl.v0) + c * kChunk, n, bar);
-    }
-  }
-  // the student's logits at the teacher's entries, before any are overwritten
-  // (dZ may be Z), and q
-  float zj = 0.0f;
-  if (id >= 0) zj = load_rw(row + id);
-  if (tid < a.k) sh.z[tid] = zj;
-  if (warp < kMaxTeacher / 32) {
-    float mx = v;  // NaN and +inf values make the row's loss NaN below
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (lane == 0) sh.red[warp] = mx;
-  }
-  __syncthreads();
-  const float vm = fmaxf(fmaxf(sh.red[0], sh.red[1]), fmaxf(sh.red[2], sh.red[3]));
-  float eq = 0.0f;
-  if (id >= 0) eq = expf((v - vm) / a.tau);
-  __syncthreads();
-  if (warp < kMaxTeacher / 32) {
-    float sq = eq;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-    if (lane == 0) sh.red[warp] = sq;
-  }
-  __syncthreads();
-  const float qsum = (sh.red[0] + sh.red[1]) + (sh.red[2] + sh.red[3]);
-  const float q = eq / qsum;
-  if (tid < a.k) sh.q[tid] = id >= 0 ? q : 0.0f;
-
-  // statistics of the row
-  Stat st = stat_none();
-  auto edge = [&](int64_t col) {
-    stat_add1<false>(st, load_rw(row + col), a.k2);
+    return t;
   };
-  if (rank == 0 && tid < sl.head) edge(tid);
-  if (sl.tail0 + tid < sl.tail1) edge(sl.tail0 + tid);
+  // chunks of the longest slice of any row
+  const int chunks = MODE == kResident
+                         ? (((int)a.V / N + ranks) / ranks * 16 + kChunk - 1) / kChunk
+                         : 0;
   if (MODE == kResident) {
-    for (int c = 0; c < chunks; ++c) {
-      if (!ptx::mbar_try_wait(ptx::smem_u32(&sh.bar[c]), 0))
-        wait_copy(ptx::smem_u32(&sh.bar[c]), a.status);
-      const int n = min(kChunk, nbytes - c * kChunk) / 16;
-      const uint4* src = reinterpret_cast<const uint4*>(buf + c * kChunk);
-      for (int i = tid; i < n; i += kDsThreads) {
-        float z[N];
-        unpack(src[i], z);
-        stat_add<false, N>(st, z, a.k2);
+    if (tid == 0) {
+      for (int c = 0; c < chunks; ++c) {
+        ptx::mbar_init(ptx::smem_u32(&sh.full[c]), 1);
+        ptx::mbar_init(ptx::smem_u32(&sh.empty[c]), THREADS / 32);
       }
+      ptx::fence_barrier_init();
+      ptx::fence_proxy_async();
     }
-  } else {
-    constexpr int U = 16 / N;
-    uint4 w[U];
-    auto fetch = [&](int64_t p) {
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int64_t k = p + (int64_t)i * kDsThreads + tid;
-        if (k < sl.v1) w[i] = MODE == kReread ? body[k] : __ldcs(body + k);
+    __syncthreads();
+    if (tid >= THREADS) {
+      // ---------------- the copies ----------------
+      int rows = 0;
+      for (int64_t t = blockIdx.x / ranks; t < a.T; t += step) {
+        bool any = false;
+        for (int j = lane; j < a.k; j += 32) {
+          const int32_t e = a.ids[t * a.k + j];
+          any |= e >= 0 && (int64_t)e < a.V && a.vals[t * a.k + j] != -inf_f();
+        }
+        if (!__any_sync(0xffffffffu, any) || (a.weights && a.weights[t] == 0.0f)) continue;
+        const E* row = Z + t * a.ld;
+        const Slice sl = slice_of(row, a.V, rank, ranks);
+        const int bytes = (sl.v1 - sl.v0) * 16;
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(row + sl.head) + (int64_t)sl.v0 * 16;
+        if (lane == 0) {
+          for (int c = 0; c < chunks; ++c) {
+            if (rows > 0) wait_phase(sh.empty[c], (uint32_t)(rows - 1) & 1u, a.status);
+            const int n = min(kChunk, bytes - c * kChunk);
+            const uint32_t bar = ptx::smem_u32(&sh.full[c]);
+            if (n <= 0) {  // (the slices of a call's rows differ by a vector)
+              ptx::mbar_arrive(bar);
+            } else {
+              ptx::mbar_expect_tx(bar, (uint32_t)n);
+              ptx::bulk_load(ptx::smem_u32(buf) + c * kChunk, src + c * kChunk, (uint32_t)n, bar);
+            }
+          }
+        }
+        __syncwarp();
+        ++rows;
+        if (ranks > 1) ptx::cluster_sync();  // the row's exchange of statistics, below
       }
-    };
-    fetch(sl.v0);
-    for (int64_t p = sl.v0; p < sl.v1; p += (int64_t)U * kDsThreads) {
-      float z[U][N];
+      if (ranks > 1) ptx::cluster_sync();
+      return;
+    }
+  }
+  // the student's logit at the entry: gathered a row ahead, and before any of
+  // the row is overwritten (dZ may be Z)
+  float z_next = 0.0f;
+  auto gather = [&](int64_t t) {
+    z_next = t < a.T && id >= 0 ? load_rw(Z + t * a.ld + id) : 0.0f;
+  };
+  entry(blockIdx.x / ranks);
+  int64_t t = next_live(blockIdx.x / ranks);
+  gather(t);
+  for (uint32_t par = 0; t < a.T; par ^= 1u) {
+    const E* row = Z + t * a.ld;
+    E* out = MODE == kLossOnly ? nullptr : dZ + t * a.ldg;
+    const Slice sl = slice_of(row, a.V, rank, ranks);
+    const uint4* body = reinterpret_cast<const uint4*>(row + sl.head);
+    const int nv = sl.v1 - sl.v0;
+    const int32_t my_id = id;
+    const float my_v = v, zj = z_next;
+    if (tid == 0) sh.scale = weight * a.tau;
+    entry(t + step);  // on its way while this row is read
+
+    // q over the kept set, up to its sum, by the first warps
+    if (warp < kMaxTeacher / 32) {
+      float mx = my_v;
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        if (p + (int64_t)i * kDsThreads + tid < sl.v1) {
-          unpack(w[i], z[i]);
-        } else {
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      if (lane == 0) sh.red[0][warp] = mx;
+    }
+    sync_threads(THREADS);
+    const float vm = fmaxf(fmaxf(sh.red[0][0], sh.red[0][1]), fmaxf(sh.red[0][2], sh.red[0][3]));
+    const float dv = (my_v - vm) / a.tau;
+    const float eq = my_id >= 0 ? expf(dv) : 0.0f;
+    if (warp < kMaxTeacher / 32) {
+      float sq = eq;
 #pragma unroll
-          for (int j = 0; j < N; ++j) z[i][j] = -inf_f();
+      for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+      if (lane == 0) sh.red[1][warp] = sq;
+      reinterpret_cast<int32_t*>(sh.id)[tid] = my_id;
+      reinterpret_cast<float*>(sh.q)[tid] = eq;
+    }
+
+    // statistics of the row
+    Stat st = stat_none();
+    if (rank == 0 && tid < sl.head) stat_add1<false>(st, load_rw(row + tid), a.k2);
+    if (sl.tail0 + tid < sl.tail1) stat_add1<false>(st, load_rw(row + sl.tail0 + tid), a.k2);
+    if (MODE == kResident) {
+      for (int c = 0; c < chunks; ++c) {
+        wait_phase(sh.full[c], par, a.status);
+        const int i = 2 * c * THREADS + tid;
+        float x[N], y[N], z[2 * N];
+        const uint4* src = reinterpret_cast<const uint4*>(buf) + i;
+        // (past the slice's end the buffer may hold anything: not read)
+        const bool two = i + THREADS < nv;
+        if (i < nv) {
+          unpack(src[0], x);
+          if (two) unpack(src[THREADS], y);
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            z[e] = x[e];
+            z[N + e] = two ? y[e] : -inf_f();
+          }
+          stat_add<false, 2 * N>(st, z, a.k2);
         }
       }
-      fetch(p + (int64_t)U * kDsThreads);
+    } else {
+      constexpr int U = 16 / N, TILE = U * THREADS;
+      constexpr int AHEAD = sizeof(E) == 4 ? 1 : 2;
+      const uint4* src = body + sl.v0 + tid;
+      uint4 w[AHEAD][U];
+      auto fetch = [&](uint4 (&x)[U], int p) {
 #pragma unroll
-      for (int i = 0; i < U; ++i) stat_add<false, N>(st, z[i], a.k2);
-    }
-  }
-  st = stat_block<false>(st, a.k2, sh.warp);
-  // (for dZ = Z, the cluster's barrier in here also orders the gathers above
-  // before the first store)
-  const Stat all = stat_cluster<false>(st, a.k2, &sh.cta, ranks);
-  const float logs = logf(all.s);  // -inf for a row of -inf: log p = -inf, loss = +inf
-
-  if (rank == 0 && a.loss && warp == 0) {
-    // entries in order, four strides of 32, then a fixed butterfly
-    float acc = 0.0f;
-    for (int j = lane; j < a.k; j += 32) {
-      const float qj = sh.q[j];
-      if (qj != 0.0f) {
-        const float lq = (a.vals[t * a.k + j] - vm) / a.tau - logf(qsum);
-        const float lp = all.s == 0.0f ? -inf_f() : (sh.z[j] - all.m) / a.tau - logs;
-        acc = fmaf(qj, lq - lp, acc);
+        for (int i = 0; i < U; ++i)
+          if (p + i * THREADS + tid < nv)
+            x[i] = MODE == kReread ? src[p + i * THREADS] : __ldcs(src + p + i * THREADS);
+      };
+#pragma unroll
+      for (int q = 0; q < AHEAD; ++q) fetch(w[q], q * TILE);
+      for (int p0 = 0; p0 < nv; p0 += AHEAD * TILE) {
+#pragma unroll
+        for (int q = 0; q < AHEAD; ++q) {
+          const int p = p0 + q * TILE;
+          if (p >= nv) break;
+          float z[16];
+#pragma unroll
+          for (int i = 0; i < U; ++i) {
+            float x[N];
+            unpack(w[q][i], x);
+            const bool there = p + i * THREADS + tid < nv;
+#pragma unroll
+            for (int e = 0; e < N; ++e) z[i * N + e] = there ? x[e] : -inf_f();
+          }
+          fetch(w[q], p + AHEAD * TILE);
+          stat_add<false, 16>(st, z, a.k2);
+        }
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (lane == 0) a.loss[t] = a.tau * a.tau * acc;
-  }
-  if (MODE != kLossOnly) {
-    const float scale = weight * a.tau;
+    st = stat_block<false>(st, a.k2, sh.warp, THREADS);
+    const Stat all = stat_cluster<false>(st, a.k2, &sh.cta[par], ranks);
+    const float scale = sh.scale;
     const float r = all.s == 0.0f ? 0.0f : scale / all.s;  // NaN rows stay NaN
     auto grad = [&](float z) { return r * ex2((z - all.m) * a.k2); };
-    auto at = [&](int64_t col) -> float {
-      const int64_t e = col - sl.head - sl.v0 * N;  // element of the slice's body
-      if (MODE == kResident && e >= 0 && e < (sl.v1 - sl.v0) * N) {
-        return load_rw(reinterpret_cast<const E*>(buf) + e);
+    // an entry's part of the loss and, of this CTA's columns, its gradient: p - q
+    // in fp32, rounded once; an id that the teacher lists twice has both weights,
+    // in list order
+    float fix = 0.0f;
+    bool mine = false;
+    if (warp < kMaxTeacher / 32) {
+      const float qsum = (sh.red[1][0] + sh.red[1][1]) + (sh.red[1][2] + sh.red[1][3]);
+      const float q = eq / qsum;
+      float part = 0.0f;
+      if (my_id >= 0 && q != 0.0f) {
+        // (log s = -inf for a row of -inf: log p = -inf, loss = +inf)
+        const float lp = all.s == 0.0f ? -inf_f() : (zj - all.m) / a.tau - logf(all.s);
+        part = q * (dv - logf(qsum) - lp);
       }
-      return load_rw(row + col);
-    };
-    if ((((uintptr_t)out ^ (uintptr_t)row) & 15) == 0) {
-      // the gradient's rows are aligned as the logits' are: whole vectors
-      uint4* dst = reinterpret_cast<uint4*>(out + sl.head) + sl.v0;
-      const uint4* src = MODE == kResident ? reinterpret_cast<const uint4*>(buf) : body + sl.v0;
-      const int64_t n = sl.v1 - sl.v0;
-      for (int64_t i = tid; i < n; i += kDsThreads) {
-        float z[N];
-        unpack(src[i], z);
 #pragma unroll
-        for (int j = 0; j < N; ++j) z[j] = grad(z[j]);
-        __stcs(dst + i, pack(z));
+      for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+      if (lane == 0) sh.loss[warp] = part;
+      const int c0 = rank == 0 ? 0 : sl.head + sl.v0 * N;
+      const int c1 = rank == ranks - 1 ? (int)a.V : sl.head + sl.v1 * N;
+      mine = MODE != kLossOnly && my_id >= 0 && my_id >= c0 && my_id < c1;
+      if (mine) {
+        float qs = 0.0f;
+        for (int j = 0; j < (a.k + 3) / 4; ++j) {
+          const int4 e = sh.id[j];
+          const float4 w = sh.q[j];
+          qs += e.x == my_id ? w.x : 0.0f;
+          qs += e.y == my_id ? w.y : 0.0f;
+          qs += e.z == my_id ? w.z : 0.0f;
+          qs += e.w == my_id ? w.w : 0.0f;
+        }
+        fix = grad(zj) - scale * (qs / qsum);
       }
-      if (rank == 0 && tid < sl.head) store_e(out + tid, grad(at(tid)));
-      if (sl.tail0 + tid < sl.tail1) store_e(out + sl.tail0 + tid, grad(at(sl.tail0 + tid)));
-    } else {
-      for (int64_t c = c0 + tid; c < c1; c += kDsThreads) store_e(out + c, grad(at(c)));
     }
-    // the teacher's entries of this CTA's columns: p - q in fp32, rounded once;
-    // an id that the teacher lists twice has both weights, in list order
-    __syncthreads();
-    if (id >= 0 && id >= c0 && id < c1) {
-      float qs = 0.0f;
-      for (int j = 0; j < a.k; ++j)
-        if (sh.id[j] == id) qs += sh.q[j];
-      store_e(out + id, grad(zj) - scale * qs);
+    // the next row's entries, and zeros for the rows left out before it
+    const int64_t tn = next_live(t + step);
+    gather(tn);
+    if (MODE != kLossOnly) {
+      auto grads = [&](const uint4& w) {
+        float z[N];
+        unpack(w, z);
+        const float2 nm = make_float2(-all.m, -all.m), kk = make_float2(a.k2, a.k2);
+        const float2 rr = make_float2(r, r);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+          const float2 x = __fmul2_rn(__fadd2_rn(make_float2(z[i], z[i + 1]), nm), kk);
+          const float2 g = __fmul2_rn(make_float2(ex2(x.x), ex2(x.y)), rr);
+          z[i] = g.x;
+          z[i + 1] = g.y;
+        }
+        return pack(z);
+      };
+      const bool aligned = (((uintptr_t)out ^ (uintptr_t)row) & 15) == 0;
+      // the edges first: their logits are in global memory
+      if (rank == 0 && tid < sl.head) store_e(out + tid, grad(load_rw(row + tid)));
+      if (sl.tail0 + tid < sl.tail1)
+        store_e(out + sl.tail0 + tid, grad(load_rw(row + sl.tail0 + tid)));
+      if (MODE == kResident) {
+        uint4* dst = reinterpret_cast<uint4*>(out + sl.head) + sl.v0;
+        for (int c = 0; c < chunks; ++c) {
+          const int i = 2 * c * THREADS + tid;
+          if (aligned) {  // the gradient's rows are aligned as the logits' are
+            const uint4* src = reinterpret_cast<const uint4*>(buf);
+            if (i < nv) __stcs(dst + i, grads(src[i]));
+            if (i + THREADS < nv) __stcs(dst + i + THREADS, grads(src[i + THREADS]));
+          } else {
+            const int e1 = min(2 * (c + 1) * THREADS, nv) * N;
+            for (int e = 2 * c * THREADS * N + tid; e < e1; e += THREADS)
+              store_e(out + sl.head + sl.v0 * N + e,
+                      grad(load_rw(reinterpret_cast<const E*>(buf) + e)));
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.empty[c]));
+        }
+      } else if (aligned) {
+        uint4* dst = reinterpret_cast<uint4*>(out + sl.head) + sl.v0;
+        for (int i = tid; i < nv; i += THREADS) __stcs(dst + i, grads(body[sl.v0 + i]));
+      } else {
+        for (int64_t e = tid; e < (int64_t)nv * N; e += THREADS)
+          store_e(out + sl.head + sl.v0 * N + e, grad(load_rw(row + sl.head + sl.v0 * N + e)));
+      }
     }
+    sync_threads(THREADS);  // the row's shared values and dense stores are done
+    if (mine) store_e(out + my_id, fix);
+    if (rank == 0 && tid == 0 && a.loss)
+      a.loss[t] = a.tau * a.tau * ((sh.loss[0] + sh.loss[1]) + (sh.loss[2] + sh.loss[3]));
+    t = tn;
   }
   if (ranks > 1) ptx::cluster_sync();  // the others' shared memory is no longer read
 }
@@ -773,8 +895,8 @@ int cluster_for(int64_t T, int64_t V, int need, int64_t tile, int sm_count) {
 }
 
 template <typename F, typename... Args>
-cudaError_t launch_rows(cudaStream_t st, F fn, int64_t T, int ranks, int threads, size_t smem,
-                        Args... args) {
+cudaError_t launch_rows(cudaStream_t st, F fn, int64_t clusters, int ranks, int threads,
+                        size_t smem, Args... args) {
   cudaError_t err = cudaSuccess;
   if (smem > 48 * 1024)
     err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -785,7 +907,7 @@ cudaError_t launch_rows(cudaStream_t st, F fn, int64_t T, int ranks, int threads
   attr[0].val.clusterDim.x = (unsigned)ranks;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)(T * ranks));
+  cfg.gridDim = dim3((unsigned)(clusters * ranks));
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -793,6 +915,27 @@ cudaError_t launch_rows(cudaStream_t st, F fn, int64_t T, int ranks, int threads
   cfg.numAttrs = 1;
   err = cudaLaunchKernelEx(&cfg, fn, args..., ranks);
   return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+template <typename F>
+cudaError_t resident_clusters(F fn, int ranks, int threads, size_t smem, int* n) {
+  cudaError_t err =
+      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ranks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)ranks);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  err = cudaOccupancyMaxActiveClusters(n, fn, &cfg);
+  if (err == cudaSuccess && *n < 1) err = cudaErrorInvalidConfiguration;
+  return err;
 }
 
 template <typename E>
@@ -807,19 +950,37 @@ cudaError_t logprobs_as(cudaStream_t st, const void* Z, int64_t T, const Logprob
 }
 
 template <typename E>
-cudaError_t distill_as(cudaStream_t st, const void* Z, void* dZ, int64_t T, const DistillArgs& a,
+cudaError_t distill_as(cudaStream_t st, const void* Z, void* dZ, const DistillArgs& a,
                        int sm_count) {
   const E* z = (const E*)Z;
   E* g = (E*)dZ;
-  const int64_t tile = (int64_t)kDsThreads * 16;
-  if (!g)
-    return launch_rows(st, k_distill<E, kLossOnly>, T, cluster_for(T, a.V, 1, tile, sm_count),
-                       kDsThreads, 0, z, g, a);
-  const int64_t need = (a.V * (int64_t)sizeof(E) + kBufBytes - 1) / kBufBytes;
+  if (!g)  // a row per CTA: the hardware hands out the next
+    return launch_rows(st, k_distill<E, kLossOnly>, a.T,
+                       cluster_for(a.T, a.V, 1, kLpThreads * 16, sm_count), kLpThreads, 0, z, g, a);
+  // a slice has at most V / N / ranks + 1 vectors
+  constexpr int64_t kVecs = kBufBytes / 16;
+  int64_t need = 1;
+  while (need <= kMaxCluster && (a.V / Vec<E>::N + need) / need > kVecs) ++need;
   if (need > kMaxCluster)
-    return launch_rows(st, k_distill<E, kReread>, T, kMaxCluster, kDsThreads, 0, z, g, a);
-  return launch_rows(st, k_distill<E, kResident>, T,
-                     cluster_for(T, a.V, (int)need, tile, sm_count), kDsThreads,
+    return launch_rows(st, k_distill<E, kReread>, a.T, kMaxCluster, kDsThreads, 0, z, g, a);
+  const int c = cluster_for(a.T, a.V, (int)need, kDsThreads * 16, sm_count);
+  int64_t clusters = a.T;
+  if (a.T * c > sm_count) {
+    // the clusters that are resident at once (a grid larger than that would work
+    // through the rest of its rows behind them): asked once per size and device
+    static std::atomic<int> known[kMaxCluster + 1][64];
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    int n = dev < 64 ? known[c][dev].load() : 0;
+    if (n == 0) {
+      err = resident_clusters(k_distill<E, kResident>, c, kDsThreads + 32, kBufBytes, &n);
+      if (err != cudaSuccess) return err;
+      if (dev < 64) known[c][dev].store(n);
+    }
+    if (n < clusters) clusters = n;
+  }
+  return launch_rows(st, k_distill<E, kResident>, clusters, c, kDsThreads + 32,
                      (size_t)kBufBytes, z, g, a);
 }
 
@@ -840,9 +1001,9 @@ cudaError_t launch_distill(cudaStream_t st, const void* Z, int dtype, int64_t T,
                            const float* weights, float* loss, void* dZ, int64_t ldg, int sm_count,
                            uint32_t* status) {
   if (T <= 0) return cudaSuccess;
-  const DistillArgs a{ld, ldg, V, ids, vals, k, tau, kLog2e / tau, weights, loss, status};
-  return dtype == DUST_BF16 ? distill_as<__nv_bfloat16>(st, Z, dZ, T, a, sm_count)
-                            : distill_as<float>(st, Z, dZ, T, a, sm_count);
+  const DistillArgs a{T, ld, ldg, V, ids, vals, k, tau, kLog2e / tau, weights, loss, status};
+  return dtype == DUST_BF16 ? distill_as<__nv_bfloat16>(st, Z, dZ, a, sm_count)
+                            : distill_as<float>(st, Z, dZ, a, sm_count);
 }
 
 }  // namespace dust
