@@ -330,7 +330,7 @@ struct LogprobArgs {
 };
 
 template <typename E, bool TOP>
-__global__ __launch_bounds__(kLpThreads, TOP ? 4 : 3) void k_token_logprobs(
+__global__ __launch_bounds__(kLpThreads, TOP || sizeof(E) == 2 ? 4 : 3) void k_token_logprobs(
     const E* __restrict__ Z, LogprobArgs a, int ranks) {
   constexpr int N = Vec<E>::N;
   // vectors per thread and tile, and tiles whose loads are in flight: 64 to 128
@@ -574,6 +574,7 @@ struct DistillShared {
 };
 
 constexpr uint64_t kCopyWaitNs = 2000000000ull;  // 2 s
+__device__ const float kOne = 1.0f;                // the weight where none are given
 
 // Wait for a phase of a barrier, for at most kCopyWaitNs: past that the call
 // reports a timeout and its outputs are unspecified. Every copy is waited for,
@@ -603,25 +604,30 @@ __global__ __launch_bounds__(MODE == kLossOnly ? kLpThreads
   __shared__ DistillShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = ranks > 1 ? (int)ptx::cluster_ctarank() : 0;
-  const int64_t step = gridDim.x / ranks;
+  // the k-th row of this cluster: one of every `step` rows, moved on by 7 from one
+  // to the next, so that a periodic mask does not leave some clusters all its rows
+  const int64_t step = gridDim.x / ranks, first = blockIdx.x / ranks;
+  auto row_of = [&](int64_t k) { return k * step + (first + 7 * k) % step; };
   // this thread's teacher entry of a row: absent (-1) where its id is -1 or its
   // value -inf
   int32_t id = -1;
   float v = -inf_f(), weight = 1.0f;
-  auto entry = [&](int64_t t) {  // as stored
-    id = -1;
-    if (t >= a.T) return;
-    weight = a.weights ? a.weights[t] : 1.0f;
-    if (tid < a.k) {
-      id = a.ids[t * a.k + tid];
-      v = a.vals[t * a.k + tid];
-    }
+  // (loaded without a condition, so that nothing waits for the values here)
+  auto entry = [&](int64_t t) {
+    if (t >= a.T) t = a.T - 1;
+    const int64_t e = t * a.k + min(tid, a.k - 1);
+    id = a.ids[e];
+    v = a.vals[e];
+    weight = *(a.weights ? a.weights + t : &kOne);
   };
-  // From row t on, whose entry is loaded, the first that is not left out (T:
-  // none). A row without a teacher entry, or of weight 0, gets zeros and its
-  // logits are not read. All CTAs of a cluster see the same rows.
-  auto next_live = [&](int64_t t) {
-    for (; t < a.T; t += step, entry(t)) {
+  // From the k-th row on, whose entry is loaded, the first that is not left out
+  // (its row T or past it: none). A row without a teacher entry, or of weight 0,
+  // gets zeros and its logits are not read. All CTAs of a cluster see the same rows.
+  auto next_live = [&](int64_t& k) {
+    for (; k * step < a.T; entry(row_of(++k))) {
+      const int64_t t = row_of(k);
+      if (t >= a.T) continue;  // (in the last, incomplete round)
+      if (tid >= a.k) id = -1;
       if (id != -1 && (id < 0 || (int64_t)id >= a.V)) {
         atomicOr(a.status, kStatusBadTarget);
         id = -1;
@@ -645,7 +651,7 @@ __global__ __launch_bounds__(MODE == kLossOnly ? kLpThreads
       }
       if (rank == 0 && tid == 0 && a.loss) a.loss[t] = 0.0f;
     }
-    return t;
+    return a.T;
   };
   // chunks of the longest slice of any row
   const int chunks = MODE == kResident
@@ -664,7 +670,9 @@ __global__ __launch_bounds__(MODE == kLossOnly ? kLpThreads
     if (tid >= THREADS) {
       // ---------------- the copies ----------------
       int rows = 0;
-      for (int64_t t = blockIdx.x / ranks; t < a.T; t += step) {
+      for (int64_t k = 0; k * step < a.T; ++k) {
+        const int64_t t = row_of(k);
+        if (t >= a.T) continue;
         bool any = false;
         for (int j = lane; j < a.k; j += 32) {
           const int32_t e = a.ids[t * a.k + j];
@@ -699,12 +707,11 @@ __global__ __launch_bounds__(MODE == kLossOnly ? kLpThreads
   // the student's logit at the entry: gathered a row ahead, and before any of
   // the row is overwritten (dZ may be Z)
   float z_next = 0.0f;
-  auto gather = [&](int64_t t) {
-    z_next = t < a.T && id >= 0 ? load_rw(Z + t * a.ld + id) : 0.0f;
-  };
-  entry(blockIdx.x / ranks);
-  int64_t t = next_live(blockIdx.x / ranks);
-  gather(t);
+  auto gather = [&](const E* row) { z_next = load_rw(row + max(id, 0)); };
+  int64_t k = 0;
+  entry(row_of(k));
+  int64_t t = next_live(k);
+  if (t < a.T) gather(Z + t * a.ld);
   for (uint32_t par = 0; t < a.T; par ^= 1u) {
     const E* row = Z + t * a.ld;
     E* out = MODE == kLossOnly ? nullptr : dZ + t * a.ldg;
@@ -714,7 +721,7 @@ __global__ __launch_bounds__(MODE == kLossOnly ? kLpThreads
     const int32_t my_id = id;
     const float my_v = v, zj = z_next;
     if (tid == 0) sh.scale = weight * a.tau;
-    entry(t + step);  // on its way while this row is read
+    entry(row_of(k + 1));  // on its way while this row is read
 
     // q over the kept set, up to its sum, by the first warps
     if (warp < kMaxTeacher / 32) {
@@ -830,8 +837,8 @@ __global__ __launch_bounds__(MODE == kLossOnly ? kLpThreads
       }
     }
     // the next row's entries, and zeros for the rows left out before it
-    const int64_t tn = next_live(t + step);
-    gather(tn);
+    const int64_t tn = next_live(++k);
+    gather(tn < a.T ? Z + tn * a.ld : row);
     if (MODE != kLossOnly) {
       auto grads = [&](const uint4& w) {
         float z[N];
