@@ -366,36 +366,42 @@ typedef struct dust_attn_dims {
   uint32_t flags;            /* DUST_FLAG_ASYNC */
   int64_t ldq, ldk, ldv, ldo, lde, lddq, lddk, lddv; /* row strides, elements */
 } dust_attn_dims;
+/* Scratch bytes of dust_attn_forward (backward 0) or dust_attn_backward (1) for
+   these dims (cu_seqlens is not read); -1 for invalid dims. Host-only. */
+int64_t dust_attn_work_bytes(const dust_attn_dims* dims, int backward);
 /* Forward.
  *   Q T x (n_heads head_dim), Kc and Vc T x (n_kv_heads head_dim)
  *   O_out   like Q; lse_out T x n_heads fp32, log-sum-exp of a row's scores
  * Rows that no sequence covers (behind the last one, say) are neither read nor
  * written, and neither is anything of one sequence mixed into another, NaN
  * included. Values that are not finite spread inside their own sequence.
- * fp32 tensors are computed in fp32. bf16 tensors: products with fp32
- * accumulation, softmax in fp32, the probabilities rounded to bf16 for the
- * product with V; outputs are rounded once.
- * Needs no scratch. lse_out must not be NULL. flags as dust_token_logprobs.
+ * fp32 tensors keep fp32 accuracy (64-wide heads run on the tensor cores in
+ * three bf16 planes per operand, other widths on CUDA cores). bf16 tensors:
+ * products with fp32 accumulation, softmax in fp32, the probabilities rounded
+ * to bf16 for the product with V; outputs are rounded once.
+ *   work     the caller's scratch, dust_attn_work_bytes(dims, 0) bytes, 256-byte
+ *            aligned, overwritten; NULL: fp32 tensors run on CUDA cores
+ * The call has no scratch of its own, so calls and captured graphs that overlap
+ * need only a work buffer each. flags as dust_token_logprobs.
  * Errors: DUST_ERR_ARG, DUST_ERR_BOUNDS (offsets that decrease, leave [0, T]
  * or make a sequence longer than max_len: that sequence is skipped),
  * DUST_ERR_TIMEOUT. */
 dust_status dust_attn_forward(dust_ctx* ctx, const dust_attn_dims* dims, const void* Q,
-                              const void* Kc, const void* Vc, void* O_out, float* lse_out);
+                              const void* Kc, const void* Vc, void* O_out, float* lse_out,
+                              void* work);
 /* Backward: gradients of sum_t <o_t, e_t>.
  *   Q, Kc, Vc, O, lse  as given to and returned by dust_attn_forward
  *   E        like Q: the error signal (gradient) at the attention output
  *   dQ_out   like Q; dK_out, dV_out like Kc (sums over the heads that share
  *            a key/value head); dtype as the inputs, rounded once
- *   delta    T x n_heads fp32 scratch of the caller, overwritten. The call
- *            has no scratch of its own, so calls and captured graphs that
- *            overlap need only a delta each.
+ *   work     as above, dust_attn_work_bytes(dims, 1) bytes, not NULL
  * The probabilities are recomputed from lse; no sum uses atomics, so results
  * are the same from run to run. Outputs must not overlap the inputs.
  * Errors as dust_attn_forward. */
 dust_status dust_attn_backward(dust_ctx* ctx, const dust_attn_dims* dims, const void* Q,
                                const void* Kc, const void* Vc, const void* O, const float* lse,
                                const void* E, void* dQ_out, void* dK_out, void* dV_out,
-                               float* delta);
+                               void* work);
 
 /* Per-stage device timing: when enabled, each call records CUDA events on
    the context's stream between its stages (clean GEMM, log-sum-exp, draws,

@@ -151,8 +151,15 @@ def test_null_contexts_and_struct_layout():
     assert L.dust_token_logprobs(None, 1, 1, 0, None, 1, None, 0, None, None, None, None, 0) == 1
     assert L.dust_distill(None, 1, 1, 0, None, 1, None, None, 1, 1.0, None, None, None, 1, 0) == 1
     d = dust.DustAttnDims()
-    assert L.dust_attn_forward(None, ctypes.byref(d), *[None] * 5) == 1
+    assert L.dust_attn_forward(None, ctypes.byref(d), *[None] * 6) == 1
     assert L.dust_attn_backward(None, ctypes.byref(d), *[None] * 10) == 1
+    assert L.dust_attn_work_bytes(ctypes.byref(d), 0) == -1
+    d = dust.DustAttnDims(T=100, n_seqs=1, max_len=100, n_heads=4, n_kv_heads=2, head_dim=64,
+                          dtype=dust.DUST_BF16)
+    assert [L.dust_attn_work_bytes(ctypes.byref(d), b) for b in (0, 1)] == [0, 1792]
+    d.dtype = dust.DUST_F32       # three bf16 planes of Q, K, V (and E)
+    assert [L.dust_attn_work_bytes(ctypes.byref(d), b) for b in (0, 1)] == [
+        100 * 64 * 6 * 8, 100 * 64 * 6 * 12 + 1792]
     # int64, pointer, int32 x6, float, uint32, int64 x8
     assert ctypes.sizeof(d) == 112 and dust.DustAttnDims.ldq.offset == 48
     assert dust.DustAttnDims.scale.offset == 40

@@ -38,7 +38,8 @@ EXPORTS = ("dust_create", "dust_set_stream", "dust_destroy", "dust_last_error",
            "dust_head_grad_noalloc", "dust_debug_bm_radius", "dust_debug_bm_angle",
            "dust_attn_grad",
            "dust_sgd_momentum", "dust_mlp_down_grad", "dust_attn_out_grad",
-           "dust_token_logprobs", "dust_distill", "dust_attn_forward", "dust_attn_backward")
+           "dust_token_logprobs", "dust_distill", "dust_attn_forward", "dust_attn_backward",
+           "dust_attn_work_bytes")
 
 
 class DustParams(ctypes.Structure):
@@ -127,7 +128,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             "dust_token_logprobs": (I32, [P, I64, I64, I32, P, I64, P, I32, P, P, P, P, U32]),
             "dust_distill": (I32, [P, I64, I64, I32, P, I64, P, P, I32, ctypes.c_float, P, P, P,
                                    I64, U32]),
-            "dust_attn_forward": (I32, [P, ctypes.POINTER(DustAttnDims), P, P, P, P, P]),
+            "dust_attn_work_bytes": (I64, [ctypes.POINTER(DustAttnDims), ctypes.c_int]),
+            "dust_attn_forward": (I32, [P, ctypes.POINTER(DustAttnDims)] + [P] * 6),
             "dust_attn_backward": (I32, [P, ctypes.POINTER(DustAttnDims)] + [P] * 10),
         }
         for name, (res, args) in sig.items():
@@ -652,9 +654,10 @@ class Context:
         else:
             out["lse"] = self._empty((dims.T, n_heads), torch.float32, Q.device)
         self._attn_call(dims, cu_seqlens, asynchronous)
+        work = self._attn_work(dims, 0, Q) if Q.dtype == torch.float32 else None
         self._check(self._L.dust_attn_forward(
             self._h, ctypes.byref(dims), Q.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(),
-            out["O"].data_ptr(), out["lse"].data_ptr()))
+            out["O"].data_ptr(), out["lse"].data_ptr(), _adr(work)))
         return out
 
     def attn_backward(self, Q, K_cache, V_cache, O, lse, E, *, n_heads, n_kv_heads=None,
@@ -682,12 +685,12 @@ class Context:
         dims.lddq = self._rows_out(out, "dQ", Q)
         dims.lddk = self._rows_out(out, "dK", K_cache)
         dims.lddv = self._rows_out(out, "dV", V_cache)
-        delta = self._empty((dims.T, n_heads), torch.float32, Q.device)
         self._attn_call(dims, cu_seqlens, asynchronous)
+        work = self._attn_work(dims, 1, Q)
         self._check(self._L.dust_attn_backward(
             self._h, ctypes.byref(dims), Q.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(),
             O.data_ptr(), lse.data_ptr(), E.data_ptr(), out["dQ"].data_ptr(),
-            out["dK"].data_ptr(), out["dV"].data_ptr(), delta.data_ptr()))
+            out["dK"].data_ptr(), out["dV"].data_ptr(), work.data_ptr()))
         return out
 
     def _rows_out(self, out: dict, key: str, like: torch.Tensor) -> int:
@@ -697,6 +700,11 @@ class Context:
             return like.shape[1]
         _check_output(out, key, like.shape, like.dtype, self.device, rows=True)
         return _row_stride(out[key], f"output {key}")
+
+    def _attn_work(self, dims: DustAttnDims, backward: int, like: torch.Tensor) -> torch.Tensor:
+        """Scratch of a call (from torch's allocator, so a captured graph has its own)."""
+        n = self._L.dust_attn_work_bytes(ctypes.byref(dims), backward)
+        return self._empty((max(n, 0),), torch.uint8, like.device)  # (-1: the call refuses dims)
 
     def _attn_call(self, dims: DustAttnDims, cu_seqlens, asynchronous: bool):
         if cu_seqlens is not None:

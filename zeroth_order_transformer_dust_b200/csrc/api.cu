@@ -348,6 +348,13 @@ dust_status check_attn_dims(dust_ctx* ctx, const dust_attn_dims* d, AttnArgs* a)
   return DUST_OK;
 }
 
+// Scratch of the exact attention calls: <o, e> per row and head, and the planes of
+// fp32 tensors where the tensor cores take them.
+bool attn_planes(const AttnArgs& a) { return a.dtype == DUST_F32 && a.head_dim == 64; }
+size_t attn_delta_bytes(const AttnArgs& a) {
+  return ((size_t)a.T * a.H * 4 + 255) / 256 * 256;
+}
+
 dust_status check_rows(dust_ctx* ctx, const AttnArgs& a, const char* name, const void* p,
                        int64_t ld, int64_t width) {
   if (a.T > 0 && !p) return fail(ctx, DUST_ERR_ARG, "%s must be non-NULL", name);
@@ -1126,8 +1133,17 @@ dust_status dust_distill(dust_ctx* ctx, int64_t T, int64_t V, int32_t dtype, con
   return finish(ctx, flags);
 }
 
+int64_t dust_attn_work_bytes(const dust_attn_dims* dims, int backward) {
+  AttnArgs a{};
+  if (check_attn_dims(nullptr, dims, &a) != DUST_OK) return -1;
+  const size_t kv = (size_t)a.T * a.Hkv * a.head_dim, q = (size_t)a.T * a.H * a.head_dim;
+  const size_t planes = attn_planes(a) ? 6 * (2 * kv + (backward ? 2 : 1) * q) : 0;
+  return (int64_t)(planes + (backward ? attn_delta_bytes(a) : 0));
+}
+
 dust_status dust_attn_forward(dust_ctx* ctx, const dust_attn_dims* dims, const void* Q,
-                              const void* Kc, const void* Vc, void* O_out, float* lse_out) {
+                              const void* Kc, const void* Vc, void* O_out, float* lse_out,
+                              void* work) {
   if (!ctx) return DUST_ERR_ARG;
   AttnArgs a{};
   DUST_TRY(check_attn_dims(ctx, dims, &a));
@@ -1137,16 +1153,18 @@ dust_status dust_attn_forward(dust_ctx* ctx, const dust_attn_dims* dims, const v
   DUST_TRY(check_rows(ctx, a, "V", Vc, a.ldv, dk));
   DUST_TRY(check_rows(ctx, a, "O", O_out, a.ldo, dq));
   if (a.T > 0 && !lse_out) return fail(ctx, DUST_ERR_ARG, "lse must be non-NULL");
-  if (!aligned(lse_out, 4)) return fail(ctx, DUST_ERR_ARG, "lse must be 4-byte aligned");
+  if (!aligned(lse_out, 4) || !aligned(work, 256))
+    return fail(ctx, DUST_ERR_ARG, "lse must be 4-byte and work 256-byte aligned");
   DUST_CU(cudaSetDevice(ctx->device));
   if (a.T == 0 || a.n_seqs == 0) return finish(ctx, dims->flags);
   a.Q = Q; a.K = Kc; a.V = Vc; a.O = O_out; a.lse_out = lse_out;
+  a.planes = attn_planes(a) ? work : nullptr;
   a.status = ctx->d_status;
   mark(ctx, nullptr);
   DUST_CU(ctx->tc_enabled && attn_exact_tc_supported(a, false)
               ? launch_attn_fwd_tc(ctx->stream, a)
               : launch_attn_exact_simt(ctx->stream, a, false));
-  ctx->launches += 1;
+  ctx->launches += a.planes ? 2 : 1;
   mark(ctx, "attn_forward");
   return finish(ctx, dims->flags);
 }
@@ -1154,7 +1172,7 @@ dust_status dust_attn_forward(dust_ctx* ctx, const dust_attn_dims* dims, const v
 dust_status dust_attn_backward(dust_ctx* ctx, const dust_attn_dims* dims, const void* Q,
                                const void* Kc, const void* Vc, const void* O, const float* lse,
                                const void* E, void* dQ_out, void* dK_out, void* dV_out,
-                               float* delta) {
+                               void* work) {
   if (!ctx) return DUST_ERR_ARG;
   AttnArgs a{};
   DUST_TRY(check_attn_dims(ctx, dims, &a));
@@ -1167,19 +1185,20 @@ dust_status dust_attn_backward(dust_ctx* ctx, const dust_attn_dims* dims, const 
   DUST_TRY(check_rows(ctx, a, "dQ", dQ_out, a.lddq, dq));
   DUST_TRY(check_rows(ctx, a, "dK", dK_out, a.lddk, dk));
   DUST_TRY(check_rows(ctx, a, "dV", dV_out, a.lddv, dk));
-  if (a.T > 0 && (!lse || !delta)) return fail(ctx, DUST_ERR_ARG, "lse and delta must be non-NULL");
-  if (!aligned(lse, 4) || !aligned(delta, 4))
-    return fail(ctx, DUST_ERR_ARG, "lse and delta must be 4-byte aligned");
+  if (a.T > 0 && (!lse || !work)) return fail(ctx, DUST_ERR_ARG, "lse and work must be non-NULL");
+  if (!aligned(lse, 4) || !aligned(work, 256))
+    return fail(ctx, DUST_ERR_ARG, "lse must be 4-byte and work 256-byte aligned");
   DUST_CU(cudaSetDevice(ctx->device));
   if (a.T == 0 || a.n_seqs == 0) return finish(ctx, dims->flags);
   a.Q = Q; a.K = Kc; a.V = Vc; a.O_in = O; a.lse = lse; a.E = E;
-  a.dQ = dQ_out; a.dK = dK_out; a.dV = dV_out; a.delta = delta;
+  a.dQ = dQ_out; a.dK = dK_out; a.dV = dV_out; a.delta = (float*)work;
+  a.planes = attn_planes(a) ? (char*)work + attn_delta_bytes(a) : nullptr;
   a.status = ctx->d_status;
   mark(ctx, nullptr);
   DUST_CU(ctx->tc_enabled && attn_exact_tc_supported(a, true)
               ? launch_attn_bwd_tc(ctx->stream, a)
               : launch_attn_exact_simt(ctx->stream, a, true));
-  ctx->launches += 2;
+  ctx->launches += a.planes ? 4 : 2;
   mark(ctx, "attn_backward");
   return finish(ctx, dims->flags);
 }

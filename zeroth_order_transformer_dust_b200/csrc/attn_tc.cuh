@@ -3,6 +3,8 @@
 #pragma once
 #include <cudaTypedefs.h>
 
+#include <type_traits>
+
 #include "internal.cuh"
 #include "tc_ptx.cuh"
 
@@ -13,6 +15,25 @@ constexpr int BM = 128;  // resident rows: TMEM lanes
 constexpr int BN = 128;  // rows of a streamed tile
 constexpr int BOX_BYTES = 128 * 64 * 2;  // a TMA box: 128 rows x 64 columns
 constexpr int SOFT_WARPS = 8;
+
+// fp32 tensors run on the tensor cores as NP = 3 bf16 planes, x = x0 + x1 + x2
+// exactly (each plane takes the next 8 significant bits; bf16 has fp32's range),
+// and a product as the six of their nine that are not below 2^-22 of it. The
+// tensor cores add to an accumulator by truncation, so the small terms go first:
+// only the last one's additions then lose anything of the sum's own size.
+// bf16 tensors are one plane, NP = 1.
+template <int NP>
+constexpr int kTerms = NP == 1 ? 1 : 6;
+template <int NP>
+__device__ constexpr int term_a(int t) {
+  constexpr int a[6] = {2, 0, 1, 0, 1, 0};
+  return NP == 1 ? 0 : a[t];
+}
+template <int NP>
+__device__ constexpr int term_b(int t) {
+  constexpr int b[6] = {0, 2, 1, 1, 0, 0};
+  return NP == 1 ? 0 : b[t];
+}
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
@@ -59,7 +80,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 __device__ __forceinline__ float inf_f() { return __int_as_float(0x7f800000); }
 
-// Columns [0, 32 n) of a thread's TMEM lane times `scale` as bf16 to dst.
+// Columns [0, 32 n) of a thread's TMEM lane times `scale` to dst.
 template <int N32>
 __device__ __forceinline__ void store_row(uint32_t taddr, float scale, __nv_bfloat16* dst,
                                           bool in) {
@@ -79,13 +100,87 @@ __device__ __forceinline__ void store_row(uint32_t taddr, float scale, __nv_bflo
     }
   }
 }
+template <int N32>
+__device__ __forceinline__ void store_row(uint32_t taddr, float scale, float* dst, bool in) {
+#pragma unroll
+  for (int c = 0; c < N32; ++c) {
+    float v[32];
+    ptx::tmem_ld32(taddr + 32 * c, v);
+    if (!in) continue;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      reinterpret_cast<float4*>(dst + 32 * c)[i] =
+          make_float4(v[4 * i] * scale, v[4 * i + 1] * scale, v[4 * i + 2] * scale,
+                      v[4 * i + 3] * scale);
+  }
+}
+template <int NP>
+using Elem = typename std::conditional<NP == 1, __nv_bfloat16, float>::type;
 
-// Zero the last `rows` rows of a landed tile (D / 64 boxes of 128 lines of 128
-// bytes; a swizzled row stays inside its line), by a warp, for the MMAs to see.
-template <int D>
+// 32 values of a row as NP bf16 planes of 16 TMEM columns: planes 0 and 1 at t and
+// t + 32 (32-column blocks of a 64-column half), plane 2 at t2. v is used up.
+template <int NP>
+__device__ __forceinline__ void store_planes(uint32_t t, uint32_t t2, float2 (&v)[16]) {
+  uint32_t pk[16];
+  if (NP == 3) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t x = __float_as_uint(v[i].x), y = __float_as_uint(v[i].y);
+        pk[i] = __byte_perm(x, y, 0x7632);  // the upper halves: truncated, so exact to take off
+        v[i].x -= __uint_as_float(x & 0xffff0000u);
+        v[i].y -= __uint_as_float(y & 0xffff0000u);
+      }
+      ptx::tmem_st16(t + 32 * q, pk);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(v[i].x, v[i].y);
+  ptx::tmem_st16(NP == 3 ? t2 : t, pk);
+}
+
+// The MMAs of S or dP: d = sum over the planes' terms of r s^T, both K-major in
+// 64-column boxes, 32 bytes per 16-deep step.
+template <int D, int NP>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t r, uint32_t s) {
+  constexpr uint32_t id = ptx::idesc_bf16_f32(BM, BN);
+  constexpr uint32_t plane = BM * D * 2;
+#pragma unroll
+  for (int t = 0; t < kTerms<NP>; ++t)
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        ptx::mma_f16(d, ptx::sdesc_kmajor_sw128(r + term_a<NP>(t) * plane + c * BOX_BYTES + 32 * k),
+                     ptx::sdesc_kmajor_sw128(s + term_b<NP>(t) * plane + c * BOX_BYTES + 32 * k), id,
+                     (t | c | k) != 0);
+}
+// The MMAs of a sum: acc += sum over the terms of (planes in TMEM as store_planes
+// left them, two halves of 64 rows of the contraction) x (tile read MN-major: 16
+// rows, 2048 bytes, per step).
+template <int D, int NP>
+__device__ __forceinline__ void mma_sum(uint32_t acc, uint32_t p, uint32_t p2, uint32_t s,
+                                        bool first) {
+  constexpr uint32_t id = ptx::idesc_bf16_f32(BM, D) | ptx::kIdescBMn;
+  constexpr uint32_t plane = BM * D * 2;
+#pragma unroll
+  for (int t = 0; t < kTerms<NP>; ++t)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t a = term_a<NP>(t) < 2 ? p + 64 * (k >> 2) + 32 * term_a<NP>(t) + 8 * (k & 3)
+                                       : p2 + 32 * (k >> 2) + 8 * (k & 3);
+      ptx::mma_f16_ts(acc, a, ptx::sdesc_mnmajor_sw128(s + term_b<NP>(t) * plane + 2048 * k, BOX_BYTES),
+                      id, !first || (t | k) != 0);
+    }
+}
+
+// Zero the last `rows` rows of a landed tile (D / 64 boxes a plane of 128 lines of
+// 128 bytes; a swizzled row stays inside its line), by a warp, for the MMAs to see.
+template <int D, int NP>
 __device__ __forceinline__ void zero_rows(uint8_t* tile, int rows, int lane) {
   uint4* t = reinterpret_cast<uint4*>(tile);
-  for (int i = lane; i < D / 64 * rows * 8; i += 32) {
+  for (int i = lane; i < NP * (D / 64) * rows * 8; i += 32) {
     const int box = i / (rows * 8), w = i % (rows * 8);
     t[box * (BOX_BYTES / 16) + (BN - rows) * 8 + w] = make_uint4(0, 0, 0, 0);
   }
@@ -117,8 +212,25 @@ bool make_map(CUtensorMap* map, const void* p, int64_t T, int64_t cols, int64_t 
 }
 
 // 16-byte rows: what TMA and the vector loads and stores need.
-bool rows16(const void* p, int64_t ld, int64_t T) {
-  return ((uintptr_t)p & 15) == 0 && (T <= 1 || (ld & 7) == 0);
+bool rows16(const AttnArgs& a, const void* p, int64_t ld) {
+  return ((uintptr_t)p & 15) == 0 && (a.T <= 1 || (ld & (a.dtype == DUST_BF16 ? 7 : 3)) == 0);
+}
+
+// The tensor maps of n tensors: of the tensors themselves (NP 1), or of their
+// planes in a.planes, which a kernel on `st` fills first (NP 3: T rows of three
+// planes side by side, tensor after tensor).
+template <int NP>
+cudaError_t make_maps(cudaStream_t st, const AttnArgs& a, const SplitSrc* src, CUtensorMap** maps,
+                      int n) {
+  __nv_bfloat16* at = (__nv_bfloat16*)a.planes;
+  for (int i = 0; i < n; ++i) {
+    const SplitSrc& x = src[i];
+    if (!(NP == 1 ? make_map(maps[i], x.p, a.T, x.width, x.ld)
+                  : make_map(maps[i], at, a.T, 3 * x.width, 3 * x.width)))
+      return cudaErrorInvalidValue;
+    at += a.T * 3 * x.width;
+  }
+  return NP == 1 ? cudaSuccess : launch_split_planes(st, src, n, a.T, a.planes);
 }
 
 }  // namespace

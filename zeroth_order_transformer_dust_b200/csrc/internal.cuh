@@ -445,6 +445,7 @@ struct AttnArgs {
   const float* lse;  // T x H, natural log (backward)
   float* lse_out;    // T x H (forward)
   float* delta;      // T x H scratch: <o, e> (backward)
+  void* planes;      // scratch of the fp32 tensor-core form, or null: the CUDA-core form
   const int32_t* cu;  // n_seqs + 1 row offsets, or null: sequences of max_len
   int64_t T;
   int n_seqs, max_len, H, Hkv, head_dim, dtype;
@@ -466,7 +467,16 @@ __device__ __forceinline__ bool attn_sequence(const AttnArgs& a, int seq, int64_
   return *beg >= 0 && *end >= *beg && *end <= a.T && *end - *beg <= a.max_len;
 }
 cudaError_t launch_attn_exact_simt(cudaStream_t st, const AttnArgs& a, bool backward);
-// Tensor cores: bf16 rows on 16-byte boundaries, head_dim 64 or 128.
+// T fp32 rows (stride ld) of each tensor as three bf16 planes side by side, x =
+// x0 + x1 + x2 with the significant bits from the top, 8 to a plane.
+struct SplitSrc {
+  const void* p;
+  int64_t ld, width;
+};
+cudaError_t launch_split_planes(cudaStream_t st, const SplitSrc* src, int n, int64_t T,
+                                void* planes);
+// Tensor cores: rows on 16-byte boundaries, bf16 with head_dim 64 or 128, or fp32
+// with 64 (planes not null).
 bool attn_exact_tc_supported(const AttnArgs& a, bool backward);
 cudaError_t launch_attn_fwd_tc(cudaStream_t st, const AttnArgs& a);
 cudaError_t launch_attn_bwd_tc(cudaStream_t st, const AttnArgs& a);

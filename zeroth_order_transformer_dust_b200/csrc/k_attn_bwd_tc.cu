@@ -1,7 +1,8 @@
-// Causal attention and its exact gradient on tensor cores (bf16 tensors, 64- or
-// 128-wide heads); formulas as in k_attn_exact.cu.
+// The exact gradient of causal attention on tensor cores (bf16 tensors with 64- or
+// 128-wide heads, fp32 tensors with 64-wide ones as three bf16 planes); formulas
+// as in k_attn_exact.cu.
 //
-// Backward. One kernel body serves both sides. A CTA keeps 128 rows of its side
+// One kernel body serves both sides. A CTA keeps 128 rows of its side
 // resident (queries with their error signal, or keys with their values) and
 // streams tiles of 128 rows of the other side. Per tile, with the resident rows
 // as TMEM lanes:
@@ -34,6 +35,12 @@
 // few keys average it out; in a sequence's first 128 rows the kernel sums
 // P dP instead, which is the same number without that rounding.
 //
+// fp32 tensors: the key side runs as two kernels, one for dV and one for dK, since
+// TMEM does not hold the third planes of P and dS and both sums. The tensor cores
+// truncate as they add, always towards zero: over a sequence of 1024 that took
+// 1.4e-5 off dK and dV. So a tile's sum starts from zero, and the softmax
+// threads add it to the total (TMEM columns too) in fp32, rounded.
+//
 // Rows at or past the end of a sequence belong to nobody or to another
 // sequence, so their content must not enter a sum, not even times 0: in the
 // one streamed tile that can hold such rows the producer overwrites them with
@@ -48,24 +55,33 @@ namespace {
 
 constexpr int THREADS = 96 + 32 * SOFT_WARPS;
 
-template <int D, bool KEY>
+// The kernels: the query side, the key side, and the key side's two gradients apart.
+enum Side { kQuery = 0, kKey = 1, kKeyV = 2, kKeyK = 3 };
+
+template <int D, int SIDE, int NP>
 struct Cfg {
-  static constexpr int NS = KEY && D == 128 ? 1 : 2;  // score buffers
-  static constexpr int ST0 = D == 64 ? 4 : (KEY ? 2 : 3);  // stages of either streamed tensor
-  static constexpr int ST1 = D == 64 ? 4 : 2;
+  static constexpr bool KEY = SIDE != kQuery;
+  static constexpr bool DV = SIDE == kKey || SIDE == kKeyV;  // sums dV
+  static constexpr bool DS = SIDE != kKeyV;                  // forms dS, sums dK or dQ
+  static constexpr int NS = (KEY && D == 128) || NP == 3 ? 1 : 2;  // score buffers
+  // stages of either streamed tensor
+  static constexpr int ST0 = NP == 3 ? 1 : (D == 64 ? 4 : (KEY ? 2 : 3));
+  static constexpr int ST1 = NP == 3 ? 1 : (D == 64 ? 4 : 2);
   static constexpr int BOXES = D / 64;                // boxes per 128 rows of a tensor
-  static constexpr int TILE_BYTES = BM * D * 2;       // 128 rows of a tensor
+  static constexpr int TILE_BYTES = NP * BM * D * 2;  // 128 rows of a tensor
   // shared memory: the resident tensors, the stages, then (key side) -lse and
   // -delta per stage of s0 or (query side) partial deltas
   static constexpr int S0 = 2 * TILE_BYTES, S1 = S0 + ST0 * TILE_BYTES;
   static constexpr int COL = S1 + ST1 * TILE_BYTES;
   static constexpr int COL_BYTES = (KEY ? ST0 : 1) * 2 * BN * 4;
   static constexpr size_t SMEM = 1024 + (size_t)COL + COL_BYTES + 256;
-  // TMEM columns: score buffers, dP, the sums
-  static constexpr int DP = NS * BN, ACC = DP + BN;
+  // TMEM columns: score buffers, dP, third planes of P and dS, the sums
+  static constexpr int DP = NS * BN, P2 = DP + BN, ACC = P2 + (NP == 3 ? 64 : 0);
+  static constexpr int TOTAL = ACC + D;  // NP 3: the sum of the tiles before
   // where a column half's dS goes, from its S columns (NS 2) or its dP columns (NS 1)
-  static constexpr int DS = KEY && NS == 2 ? 32 : 0;
-  static_assert(ACC + (KEY ? 2 : 1) * D <= 512, "TMEM columns");
+  static constexpr int DS_AT = KEY && NS == 2 ? 32 : 0;
+  static_assert(ACC + (SIDE == kKey || NP == 3 ? 2 : 1) * D <= 512, "TMEM columns");
+  static_assert(NP == 1 || SIDE != kKey, "one sum at a time");
   static_assert(SMEM <= 227 * 1024 && COL_BYTES >= 2 * BM * 4, "shared memory");
 };
 
@@ -80,12 +96,14 @@ static_assert(sizeof(Bars) <= 256, "barrier block");
 // Resident tensors r0, r1 and streamed tensors s0, s1 of the score products
 // S = r0 s0^T and dP = r1 s1^T: (Q, E; K, V) on the query side, (K, V; Q, E) on
 // the key side.
-template <int D, bool KEY>
-__global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
+template <int D, int SIDE, int NP>
+__global__ __launch_bounds__(THREADS, 1) void k_attn_bwd_tc(
     const __grid_constant__ CUtensorMap tmR0, const __grid_constant__ CUtensorMap tmR1,
     const __grid_constant__ CUtensorMap tmS0, const __grid_constant__ CUtensorMap tmS1,
     AttnArgs a) {
-  using C = Cfg<D, KEY>;
+  using C = Cfg<D, SIDE, NP>;
+  constexpr bool KEY = C::KEY, DV = C::DV, DS = C::DS;
+  using E = Elem<NP>;
   constexpr int NS = C::NS, ST0 = C::ST0, ST1 = C::ST1;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
@@ -115,6 +133,8 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
   const int per_head = KEY ? (len + BN - 1) / BN - tile : tile + 1;
   const int n = KEY ? group * per_head : per_head;
   const int s_off = KEY ? tile : 0;
+  // columns between the planes of the resident and the streamed tensors
+  const int r_plane = heads * D, s_plane = (KEY ? a.H : a.Hkv) * D;
 
   if (threadIdx.x == 0) {
     ptx::mbar_init(ptx::smem_u32(&sh->res), 1);
@@ -139,11 +159,12 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
     ptx::fence_proxy_async();
     // the resident rows are on their way while TMEM is allocated
     const uint32_t bar = ptx::smem_u32(&sh->res);
-    ptx::mbar_expect_tx(bar, 2 * C::TILE_BYTES);
-    for (int t = 0; t < 2; ++t)
-      for (int c = 0; c < C::BOXES; ++c)
+    ptx::mbar_expect_tx(bar, (DS ? 2 : 1) * C::TILE_BYTES);
+    for (int t = 0; t < (DS ? 2 : 1); ++t)
+      for (int c = 0; c < NP * C::BOXES; ++c)
         ptx::tma_load_2d(base + t * C::TILE_BYTES + c * BOX_BYTES, t ? &tmR1 : &tmR0,
-                         head * D + 64 * c, (int)(beg + r_first), bar);
+                         c / C::BOXES * r_plane + head * D + 64 * (c % C::BOXES),
+                         (int)(beg + r_first), bar);
   }
   if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_u32(&sh->tmem_base), 512);
@@ -171,7 +192,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
         const int q = r + lane + 32 * i;
         const bool in = j < n && q < len;
         nl[i] = in ? -a.lse[(beg + q) * a.H + h] * kLog2e : -inf_f();
-        nd[i] = in ? -a.delta[(beg + q) * a.H + h] : 0.0f;
+        nd[i] = DS && in ? -a.delta[(beg + q) * a.H + h] : 0.0f;
       }
     };
     if (KEY) fetch_cols(0);
@@ -191,9 +212,10 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
       if (lane == 0) {
         const uint32_t bar = partial ? land : fb;
         ptx::mbar_expect_tx(bar, C::TILE_BYTES);
-        for (int c = 0; c < C::BOXES; ++c)
-          ptx::tma_load_2d(base + off + st * C::TILE_BYTES + c * BOX_BYTES, map, h * D + 64 * c,
-                           (int)(beg + r), bar);
+        for (int c = 0; c < NP * C::BOXES; ++c)
+          ptx::tma_load_2d(base + off + st * C::TILE_BYTES + c * BOX_BYTES, map,
+                           c / C::BOXES * s_plane + h * D + 64 * (c % C::BOXES), (int)(beg + r),
+                           bar);
       }
       *armed = j + 1;
       if (KEY && off == C::S0) {
@@ -208,7 +230,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
       if (partial) {
         if (!wait_warp(land, land_phase, abort, a.status)) return false;
         land_phase ^= 1u;
-        zero_rows<D>(basep + off + st * C::TILE_BYTES, r + BN - len, lane);
+        zero_rows<D, NP>(basep + off + st * C::TILE_BYTES, r + BN - len, lane);
       }
       __syncwarp();
       if (lane == 0) {
@@ -241,42 +263,35 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
   } else if (warp == 1) {
     // ---------------- score products: S and dP ----------------
     if (lane == 0) {
-      constexpr uint32_t id = ptx::idesc_bf16_f32(BM, BN);
-      // K-major operands, 64-column boxes, 32 bytes per 16-deep step
-      auto product = [&](uint32_t d, uint32_t r, uint32_t s) {
-        ptx::tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < C::BOXES; ++c)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            ptx::mma_f16(d, ptx::sdesc_kmajor_sw128(r + c * BOX_BYTES + 32 * k),
-                         ptx::sdesc_kmajor_sw128(s + c * BOX_BYTES + 32 * k), id, (c | k) != 0);
-      };
       bool issued = false;
       auto s_product = [&](int j) {
         if (!wait(sh->full0[j % ST0], j / ST0)) return false;
-        product(tmem + (j % NS) * BN, base, base + C::S0 + (j % ST0) * C::TILE_BYTES);
+        ptx::tc_fence_after();
+        mma_scores<D, NP>(tmem + (j % NS) * BN, base, base + C::S0 + (j % ST0) * C::TILE_BYTES);
         ptx::mma_commit(ptx::smem_u32(&sh->sfull[j % NS]));
         issued = true;
         return true;
       };
       auto dp_product = [&](int j) {
         if (!wait(sh->full1[j % ST1], j / ST1)) return false;
-        product(tmem + C::DP, base + C::TILE_BYTES, base + C::S1 + (j % ST1) * C::TILE_BYTES);
+        ptx::tc_fence_after();
+        mma_scores<D, NP>(tmem + C::DP, base + C::TILE_BYTES,
+                          base + C::S1 + (j % ST1) * C::TILE_BYTES);
         ptx::mma_commit(ptx::smem_u32(&sh->dpfull));
-        if (!KEY) ptx::mma_commit(ptx::smem_u32(&sh->empty1[j % ST1]));
+        if (!DV) ptx::mma_commit(ptx::smem_u32(&sh->empty1[j % ST1]));
         return true;
       };
       // the gradient MMAs of tile j are complete
       auto done0 = [&](int j) { return wait(sh->empty0[j % ST0], j / ST0); };
-      bool ok = wait(sh->res, 0) && s_product(0) && dp_product(0);
+      bool ok = wait(sh->res, 0) && s_product(0) && (!DS || dp_product(0));
       if (NS == 2 && n > 1) ok = ok && s_product(1);
       for (int j = 0; j + 1 < n && ok; ++j) {
         if (NS == 2)  // dP's columns are read once dS is there; S's free after the tile's MMAs
           ok = wait(sh->dsfull[j & 1], j >> 1) && dp_product(j + 1) &&
                (j + 2 >= n || (done0(j) && s_product(j + 2)));
-        else          // S's columns are free after dV's MMAs, dP's after dK's
-          ok = wait(sh->vdone, j) && s_product(j + 1) && done0(j) && dp_product(j + 1);
+        else  // S's columns are free after dV's MMAs (no dV: once read), dP's after dK's
+          ok = (DV ? wait(sh->vdone, j) : wait(sh->dsfull[j & 1], j >> 1)) && s_product(j + 1) &&
+               (!DS || (done0(j) && dp_product(j + 1)));
       }
       if (issued) {  // complete before TMEM is released
         int dummy = 0;
@@ -287,34 +302,31 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
   } else if (warp == 2 + SOFT_WARPS) {
     // ---------------- gradient products ----------------
     if (lane == 0) {
-      constexpr uint32_t id = ptx::idesc_bf16_f32(BM, D) | ptx::kIdescBMn;
-      // sum += (bf16 tile in TMEM) x (streamed tile read MN-major: 16 rows, 2048
-      // bytes, per step). The softmax warps of column half h left their 64
-      // columns at 64 h: four steps each.
-      auto gradient = [&](uint32_t acc, uint32_t p, uint32_t s, bool first) {
-        ptx::tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          ptx::mma_f16_ts(acc, p + 64 * (k >> 2) + 8 * (k & 3),
-                          ptx::sdesc_mnmajor_sw128(s + 2048 * k, BOX_BYTES), id, !first || k != 0);
-      };
       const uint32_t acc0 = tmem + C::ACC, acc1 = acc0 + D;
       bool issued = false;
       for (int j = 0; j < n; ++j) {
         const uint32_t s_at = tmem + (j % NS) * BN;
         // (P needs only s0's tile: s1's is waited for here, too)
-        if (KEY) {  // dV += P^T E
+        if (DV) {  // dV += P^T E
           if (!wait(sh->full1[j % ST1], j / ST1) || !wait(sh->pfull[j & 1], j >> 1)) break;
-          gradient(acc0, s_at, base + C::S1 + (j % ST1) * C::TILE_BYTES, j == 0);
+          ptx::tc_fence_after();
+          mma_sum<D, NP>(acc0, s_at, tmem + C::P2, base + C::S1 + (j % ST1) * C::TILE_BYTES,
+                         NP == 3 || j == 0);
           ptx::mma_commit(ptx::smem_u32(&sh->vdone));
+          if (!DS) {  // (s0's stage too only here: its lse is read for P)
+            ptx::mma_commit(ptx::smem_u32(&sh->empty0[j % ST0]));
+            ptx::mma_commit(ptx::smem_u32(&sh->empty1[j % ST1]));
+          }
           issued = true;
         }
+        if (!DS) continue;
         // dK += dS^T Q, dQ += dS K; dS also means that dP's MMAs are done with s1's tile
         if (!wait(sh->full0[j % ST0], j / ST0) || !wait(sh->dsfull[j & 1], j >> 1)) break;
-        gradient(KEY ? acc1 : acc0, (NS == 2 ? s_at : tmem + C::DP) + C::DS,
-                 base + C::S0 + (j % ST0) * C::TILE_BYTES, j == 0);
+        ptx::tc_fence_after();
+        mma_sum<D, NP>(DV ? acc1 : acc0, (NS == 2 ? s_at : tmem + C::DP) + C::DS_AT, tmem + C::P2,
+                       base + C::S0 + (j % ST0) * C::TILE_BYTES, NP == 3 || j == 0);
         ptx::mma_commit(ptx::smem_u32(&sh->empty0[j % ST0]));
-        if (KEY) ptx::mma_commit(ptx::smem_u32(&sh->empty1[j % ST1]));
+        if (DV) ptx::mma_commit(ptx::smem_u32(&sh->empty1[j % ST1]));
         issued = true;
       }
       if (issued) {  // complete before the sums are read, or TMEM is released
@@ -345,25 +357,50 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
         float d = 0.0f;
         if (in) {
           const int64_t r = beg + rr;
-          const uint4* o = reinterpret_cast<const uint4*>(
-              (const __nv_bfloat16*)a.O_in + r * a.ldo + head * D + half * (D / 2));
-          const uint4* e = reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.E + r * a.lde +
-                                                          head * D + half * (D / 2));
+          const uint4* o =
+              reinterpret_cast<const uint4*>((const E*)a.O_in + r * a.ldo + head * D + half * (D / 2));
+          const uint4* e =
+              reinterpret_cast<const uint4*>((const E*)a.E + r * a.lde + head * D + half * (D / 2));
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
+          for (int i = 0; i < D / 2 * (int)sizeof(E) / 16; ++i) {
             const uint4 x = __ldg(o + i), y = __ldg(e + i);
             const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              d = fmaf(__uint_as_float(xs[w] << 16), __uint_as_float(ys[w] << 16), d);
-              d = fmaf(__uint_as_float(xs[w] & 0xffff0000u),
-                       __uint_as_float(ys[w] & 0xffff0000u), d);
+              if (NP == 1) {
+                d = fmaf(__uint_as_float(xs[w] << 16), __uint_as_float(ys[w] << 16), d);
+                d = fmaf(__uint_as_float(xs[w] & 0xffff0000u),
+                         __uint_as_float(ys[w] & 0xffff0000u), d);
+              } else {
+                d = fmaf(__uint_as_float(xs[w]), __uint_as_float(ys[w]), d);
+              }
             }
           }
         }
         ndelta = -row_sum(d);
       }
     }
+    // NP 3: total += the sum of tile j, whose MMAs are waited for; this thread's half
+    // of the row's columns
+    const uint32_t acc = lane_base + C::ACC + half * (D / 2);
+    auto flush = [&](int j) {
+      uint64_t& bar = DS ? sh->empty0[j % ST0] : sh->vdone;
+      if (!wait_warp(ptx::smem_u32(&bar), (uint32_t)(j / (DS ? ST0 : 1)) & 1u, abort, a.status))
+        return false;
+      ptx::tc_fence_after();
+      uint32_t x[32], y[32], w[16];
+      ptx::tmem_ld32x2(acc, x, lane_base + C::TOTAL + half * (D / 2), y);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          w[i] = j == 0 ? x[16 * b + i]
+                        : __float_as_uint(__uint_as_float(x[16 * b + i]) +
+                                          __uint_as_float(y[16 * b + i]));
+        ptx::tmem_st16(lane_base + C::TOTAL + half * (D / 2) + 16 * b, w);
+      }
+      return true;
+    };
     bool ok = true, summed = KEY || tile > 0;
     for (int j = 0; j < n; ++j) {
       const int b = j % NS, st = j % ST0;
@@ -387,7 +424,6 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
               s[i >> 5][i & 31] = 0xff800000u;  // -inf: p = 0
         }
         const float2 cc = make_float2(c2, c2);
-        uint32_t pk[16];
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
           float4 l4 = make_float4(nlse2, nlse2, nlse2, nlse2);
@@ -399,18 +435,26 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
                                                     __uint_as_float(s[e >> 5][(e & 31) + 1])),
                                         cc, k ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y));
             p[i + k] = make_float2(ex2(x.x), ex2(x.y));
-            if (KEY) pk[(i + k) & 15] = pack_bf16(p[i + k].x, p[i + k].y);
           }
-          if (KEY && (i & 15) == 14) ptx::tmem_st16(ts + (i & 16), pk);
+          if (DV && (i & 15) == 14) {
+            float2 v[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = p[(i & 16) + k];
+            store_planes<NP>(ts + (i & 16), lane_base + C::P2 + 32 * half + (i & 16), v);
+          }
         }
-        if (KEY) {
+        if (DV) {
+          if (NP == 3 && j > 0 && !flush(j - 1)) {
+            ok = false;
+            break;
+          }
           ptx::tmem_wait_st();
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh->pfull[j & 1]));
         }
       }
-      {  // dS from P and dP
+      if (DS) {  // dS from P and dP
         ok = wait_warp(ptx::smem_u32(&sh->dpfull), (uint32_t)j & 1u, abort, a.status);
         if (!ok) break;
         ptx::tc_fence_after();
@@ -429,19 +473,26 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
           ndelta = -row_sum(acc.x + acc.y);
           summed = true;
         }
-        uint32_t pk[16];
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          float4 d4 = make_float4(ndelta, ndelta, ndelta, ndelta);
-          if (KEY) d4 = *reinterpret_cast<const float4*>(cl + BN + 2 * i);
+        for (int h = 0; h < 2; ++h) {
+          float2 v[16];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float2 ds = __fmul2_rn(
-                p[i + k], __fadd2_rn(dpair(i + k), k ? make_float2(d4.z, d4.w)
-                                                     : make_float2(d4.x, d4.y)));
-            pk[(i + k) & 15] = pack_bf16(ds.x, ds.y);
+          for (int i = 0; i < 16; i += 2) {
+            float4 d4 = make_float4(ndelta, ndelta, ndelta, ndelta);
+            if (KEY) d4 = *reinterpret_cast<const float4*>(cl + BN + 32 * h + 2 * i);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              v[i + k] = __fmul2_rn(
+                  p[16 * h + i + k],
+                  __fadd2_rn(dpair(16 * h + i + k),
+                             k ? make_float2(d4.z, d4.w) : make_float2(d4.x, d4.y)));
           }
-          if ((i & 15) == 14) ptx::tmem_st16((NS == 2 ? ts : td) + C::DS + (i & 16), pk);
+          store_planes<NP>((NS == 2 ? ts : td) + C::DS_AT + 16 * h,
+                           lane_base + C::P2 + 32 * half + 16 * h, v);
+        }
+        if (NP == 3 && j > 0 && !flush(j - 1)) {
+          ok = false;
+          break;
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
@@ -453,16 +504,22 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
     if (!summed) asm volatile("bar.arrive 1, %0;" ::"n"(32 * SOFT_WARPS) : "memory");
     if (!KEY && in && half == 0) a.delta[(beg + rr) * a.H + head] = -ndelta;
     if (ok) ok = wait_warp(ptx::smem_u32(&sh->afull), 0, abort, a.status);
+    if (NP == 3 && ok) ok = flush(n - 1);
+    if (NP == 3) ptx::tmem_wait_st();
     if (ok && !*abort) {
       ptx::tc_fence_after();
-      const uint32_t acc = lane_base + C::ACC + half * (D / 2);
+      const uint32_t sum = NP == 3 ? acc + D : acc;  // (TOTAL, or the accumulator)
       const int64_t r = beg + rr;
       const int64_t col = (int64_t)head * D + half * (D / 2);
-      if (KEY) {
-        store_row<D / 64>(acc, 1.0f, (__nv_bfloat16*)a.dV + r * a.lddv + col, in);
-        store_row<D / 64>(acc + D, a.scale, (__nv_bfloat16*)a.dK + r * a.lddk + col, in);
+      if (SIDE == kKey) {
+        store_row<D / 64>(sum, 1.0f, (E*)a.dV + r * a.lddv + col, in);
+        store_row<D / 64>(sum + D, a.scale, (E*)a.dK + r * a.lddk + col, in);
+      } else if (SIDE == kKeyV) {
+        store_row<D / 64>(sum, 1.0f, (E*)a.dV + r * a.lddv + col, in);
+      } else if (SIDE == kKeyK) {
+        store_row<D / 64>(sum, a.scale, (E*)a.dK + r * a.lddk + col, in);
       } else {
-        store_row<D / 64>(acc, a.scale, (__nv_bfloat16*)a.dQ + r * a.lddq + col, in);
+        store_row<D / 64>(sum, a.scale, (E*)a.dQ + r * a.lddq + col, in);
       }
     }
   }
@@ -473,46 +530,56 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_exact_bwd_tc(
   if (warp == 1) ptx::tmem_dealloc(tmem, 512);
 }
 
-template <int D, bool KEY>
+template <int D, int SIDE, int NP>
 cudaError_t launch_side(cudaStream_t st, const AttnArgs& a, const CUtensorMap& q,
                         const CUtensorMap& e, const CUtensorMap& k, const CUtensorMap& v) {
-  auto fn = k_attn_exact_bwd_tc<D, KEY>;
-  const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)Cfg<D, KEY>::SMEM);
+  auto fn = k_attn_bwd_tc<D, SIDE, NP>;
+  constexpr bool KEY = SIDE != kQuery;
+  constexpr size_t smem = Cfg<D, SIDE, NP>::SMEM;
+  const cudaError_t err =
+      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   const dim3 grid((unsigned)(KEY ? a.Hkv : a.H) * (unsigned)a.n_seqs,
                   (unsigned)((a.max_len + BM - 1) / BM));
   if (KEY)
-    fn<<<grid, THREADS, Cfg<D, KEY>::SMEM, st>>>(k, v, q, e, a);
+    fn<<<grid, THREADS, smem, st>>>(k, v, q, e, a);
   else
-    fn<<<grid, THREADS, Cfg<D, KEY>::SMEM, st>>>(q, e, k, v, a);
+    fn<<<grid, THREADS, smem, st>>>(q, e, k, v, a);
   return cudaGetLastError();
 }
 
-template <int D>
+template <int D, int NP>
 cudaError_t backward_as(cudaStream_t st, const AttnArgs& a) {
   CUtensorMap q, e, k, v;
   const int64_t wq = (int64_t)a.H * D, wk = (int64_t)a.Hkv * D;
-  if (!make_map(&q, a.Q, a.T, wq, a.ldq) || !make_map(&e, a.E, a.T, wq, a.lde) ||
-      !make_map(&k, a.K, a.T, wk, a.ldk) || !make_map(&v, a.V, a.T, wk, a.ldv))
-    return cudaErrorInvalidValue;
-  const cudaError_t err = launch_side<D, false>(st, a, q, e, k, v);
-  if (err != cudaSuccess) return err;
-  return launch_side<D, true>(st, a, q, e, k, v);
+  const SplitSrc src[4] = {{a.Q, a.ldq, wq}, {a.E, a.lde, wq}, {a.K, a.ldk, wk}, {a.V, a.ldv, wk}};
+  CUtensorMap* maps[4] = {&q, &e, &k, &v};
+  cudaError_t err = make_maps<NP>(st, a, src, maps, 4);
+  if (err == cudaSuccess) err = launch_side<D, kQuery, NP>(st, a, q, e, k, v);
+  if constexpr (NP == 1) {
+    if (err == cudaSuccess) err = launch_side<D, kKey, NP>(st, a, q, e, k, v);
+  } else {
+    if (err == cudaSuccess) err = launch_side<D, kKeyV, NP>(st, a, q, e, k, v);
+    if (err == cudaSuccess) err = launch_side<D, kKeyK, NP>(st, a, q, e, k, v);
+  }
+  return err;
 }
 
 }  // namespace
 
 bool attn_exact_tc_supported(const AttnArgs& a, bool backward) {
-  if (a.dtype != DUST_BF16 || (a.head_dim != 64 && a.head_dim != 128) || !encode_fn()) return false;
-  if (!rows16(a.Q, a.ldq, a.T) || !rows16(a.K, a.ldk, a.T) || !rows16(a.V, a.ldv, a.T)) return false;
-  if (!backward) return rows16(a.O, a.ldo, a.T);
-  return rows16(a.O_in, a.ldo, a.T) && rows16(a.E, a.lde, a.T) && rows16(a.dQ, a.lddq, a.T) &&
-         rows16(a.dK, a.lddk, a.T) && rows16(a.dV, a.lddv, a.T);
+  const bool heads = a.dtype == DUST_BF16 ? a.head_dim == 64 || a.head_dim == 128
+                                          : a.head_dim == 64 && a.planes;
+  if (!heads || !encode_fn()) return false;
+  if (!rows16(a, a.Q, a.ldq) || !rows16(a, a.K, a.ldk) || !rows16(a, a.V, a.ldv)) return false;
+  if (!backward) return rows16(a, a.O, a.ldo);
+  return rows16(a, a.O_in, a.ldo) && rows16(a, a.E, a.lde) && rows16(a, a.dQ, a.lddq) &&
+         rows16(a, a.dK, a.lddk) && rows16(a, a.dV, a.lddv);
 }
 
 cudaError_t launch_attn_bwd_tc(cudaStream_t st, const AttnArgs& a) {
-  return a.head_dim == 64 ? backward_as<64>(st, a) : backward_as<128>(st, a);
+  if (a.dtype == DUST_F32) return backward_as<64, 3>(st, a);
+  return a.head_dim == 64 ? backward_as<64, 1>(st, a) : backward_as<128, 1>(st, a);
 }
 
 }  // namespace dust

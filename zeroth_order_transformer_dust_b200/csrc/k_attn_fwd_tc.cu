@@ -1,5 +1,6 @@
-// Causal attention on tensor cores (bf16 tensors, 64- or 128-wide heads): the
-// forward pass of the exact attention; formulas as in k_attn_exact.cu.
+// Causal attention on tensor cores (bf16 tensors with 64- or 128-wide heads, fp32
+// tensors with 64-wide ones as three bf16 planes): the forward pass of the exact
+// attention; formulas as in k_attn_exact.cu.
 //
 // A CTA owns 256 query rows of a head as two tiles of 128 and streams key/value
 // tiles of 128 rows. Per streamed tile and query tile g, with the query rows as
@@ -27,16 +28,17 @@ namespace {
 constexpr int THREADS = 128 + 32 * SOFT_WARPS;
 constexpr float kGrow = 8.0f;  // log2 growth of a row's maximum that rescales O
 
-template <int D>
+template <int D, int NP>
 struct Cfg {
-  static constexpr int STK = D == 64 ? 4 : 3, STV = D == 64 ? 4 : 2;  // key, value stages
+  // key and value stages
+  static constexpr int STK = NP == 3 ? 1 : (D == 64 ? 4 : 3), STV = NP == 3 ? 1 : (D == 64 ? 4 : 2);
   static constexpr int BOXES = D / 64;
-  static constexpr int TILE_BYTES = BM * D * 2;
+  static constexpr int TILE_BYTES = NP * BM * D * 2;
   static constexpr int K0 = 2 * TILE_BYTES, V0 = K0 + STK * TILE_BYTES;
   static constexpr int BARS = V0 + STV * TILE_BYTES;
   static constexpr size_t SMEM = 1024 + (size_t)BARS + 256;
-  static constexpr int O = 2 * BN;  // TMEM: S_0, S_1, O_0, O_1
-  static_assert(O + 2 * D <= 512, "TMEM columns");
+  static constexpr int O = 2 * BN, P2 = O + 2 * D;  // TMEM: S_0, S_1, O_0, O_1, third planes of P
+  static_assert(P2 + (NP == 3 ? 128 : 0) <= 512, "TMEM columns");
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -48,11 +50,12 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
 
-template <int D>
+template <int D, int NP>
 __global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
     const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
     const __grid_constant__ CUtensorMap tmV, AttnArgs a) {
-  using C = Cfg<D>;
+  using C = Cfg<D, NP>;
+  using E = Elem<NP>;
   constexpr int STK = C::STK, STV = C::STV;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
@@ -100,8 +103,9 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
     for (int g = 0; g < (n1 ? 2 : 1); ++g) {
       const uint32_t bar = ptx::smem_u32(&sh->res[g]);
       ptx::mbar_expect_tx(bar, C::TILE_BYTES);
-      for (int c = 0; c < C::BOXES; ++c)
-        ptx::tma_load_2d(base + g * C::TILE_BYTES + c * BOX_BYTES, &tmQ, head * D + 64 * c,
+      for (int c = 0; c < NP * C::BOXES; ++c)
+        ptx::tma_load_2d(base + g * C::TILE_BYTES + c * BOX_BYTES, &tmQ,
+                         c / C::BOXES * a.H * D + head * D + 64 * (c % C::BOXES),
                          (int)(beg + r_first + g * BM), bar);
     }
   }
@@ -133,15 +137,16 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
       if (lane == 0) {
         const uint32_t bar = partial ? land : fb;
         ptx::mbar_expect_tx(bar, C::TILE_BYTES);
-        for (int c = 0; c < C::BOXES; ++c)
-          ptx::tma_load_2d(base + off + st * C::TILE_BYTES + c * BOX_BYTES, map, hk * D + 64 * c,
+        for (int c = 0; c < NP * C::BOXES; ++c)
+          ptx::tma_load_2d(base + off + st * C::TILE_BYTES + c * BOX_BYTES, map,
+                           c / C::BOXES * a.Hkv * D + hk * D + 64 * (c % C::BOXES),
                            (int)(beg + j * BN), bar);
       }
       *armed = j + 1;
       if (partial) {
         if (!wait_warp(land, land_phase, abort, a.status)) return false;
         land_phase ^= 1u;
-        zero_rows<D>(basep + off + st * C::TILE_BYTES, (j + 1) * BN - len, lane);
+        zero_rows<D, NP>(basep + off + st * C::TILE_BYTES, (j + 1) * BN - len, lane);
       }
       __syncwarp();
       if (lane == 0) {
@@ -175,7 +180,6 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
   } else if (warp == 1) {
     // ---------------- S_g = Q_g K^T ----------------
     if (lane == 0) {
-      constexpr uint32_t id = ptx::idesc_bf16_f32(BM, BN);
       bool issued = false, ok = true;
       for (int j = 0; j < n && ok; ++j) {
         ok = wait(sh->kfull[j % STK], j / STK);
@@ -185,14 +189,8 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
           ok = j == 0 ? wait(sh->res[g], 0) : wait(sh->odone[g], j - 1);
           if (!ok) break;
           ptx::tc_fence_after();
-          const uint32_t q = base + g * C::TILE_BYTES;
-          const uint32_t k = base + C::K0 + (j % STK) * C::TILE_BYTES;
-#pragma unroll
-          for (int c = 0; c < C::BOXES; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              ptx::mma_f16(tmem + g * BN, ptx::sdesc_kmajor_sw128(q + c * BOX_BYTES + 32 * i),
-                           ptx::sdesc_kmajor_sw128(k + c * BOX_BYTES + 32 * i), id, (c | i) != 0);
+          mma_scores<D, NP>(tmem + g * BN, base + g * C::TILE_BYTES,
+                            base + C::K0 + (j % STK) * C::TILE_BYTES);
           ptx::mma_commit(ptx::smem_u32(&sh->sfull[g]));
           issued = true;
         }
@@ -207,7 +205,6 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
   } else if (warp == 2) {
     // ---------------- O_g += P_g V ----------------
     if (lane == 0) {
-      constexpr uint32_t id = ptx::idesc_bf16_f32(BM, D) | ptx::kIdescBMn;
       bool ok = true;
       for (int j = 0; j < n && ok; ++j) {
         ok = wait(sh->vfull[j % STV], j / STV);
@@ -216,11 +213,8 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
           ok = wait(sh->pfull[g], j);
           if (!ok) break;
           ptx::tc_fence_after();
-          const uint32_t v = base + C::V0 + (j % STV) * C::TILE_BYTES;
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            ptx::mma_f16_ts(tmem + C::O + g * D, tmem + g * BN + 8 * i,
-                            ptx::sdesc_mnmajor_sw128(v + 2048 * i, BOX_BYTES), id, (j | i) != 0);
+          mma_sum<D, NP>(tmem + C::O + g * D, tmem + g * BN, tmem + C::P2 + 64 * g,
+                         base + C::V0 + (j % STV) * C::TILE_BYTES, j == 0);
           ptx::mma_commit(ptx::smem_u32(&sh->odone[g]));
         }
         if (ok) ptx::mma_commit(ptx::smem_u32(&sh->vempty[j % STV]));
@@ -290,18 +284,19 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (h == 1) load(1);  // (the first half is still in registers)
-        uint32_t pk[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int e = 2 * i;
-          const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[e >> 5][e & 31]),
-                                                  __uint_as_float(s[e >> 5][(e & 31) + 1])),
-                                      cc, nm);
-          const float2 p = make_float2(ex2(x.x), ex2(x.y));
-          sum[i & 1] = __fadd2_rn(sum[i & 1], p);
-          pk[i & 15] = pack_bf16(p.x, p.y);
+        for (int b = 0; b < 2; ++b) {
+          float2 v[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[b][2 * i]),
+                                                    __uint_as_float(s[b][2 * i + 1])),
+                                        cc, nm);
+            v[i] = make_float2(ex2(x.x), ex2(x.y));
+            sum[i & 1] = __fadd2_rn(sum[i & 1], v[i]);
+          }
           // P's columns lie over those of S that this thread has read
-          if ((i & 15) == 15) ptx::tmem_st16(ts + 32 * h + (i & 16), pk);
+          store_planes<NP>(ts + 64 * h + 16 * b, lane_base + C::P2 + 64 * g + 32 * h + 16 * b, v);
         }
       }
       l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
@@ -316,7 +311,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
       ptx::tc_fence_after();
       const int64_t r = beg + rr;
       if (in) a.lse_out[r * a.H + head] = 0.6931471805599453f * m + logf(l);
-      store_row<D / 32>(to, 1.0f / l, (__nv_bfloat16*)a.O + r * a.ldo + (int64_t)head * D, in);
+      store_row<D / 32>(to, 1.0f / l, (E*)a.O + r * a.ldo + (int64_t)head * D, in);
     }
   }
 
@@ -326,27 +321,29 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
   if (warp == 1) ptx::tmem_dealloc(tmem, 512);
 }
 
-template <int D>
+template <int D, int NP>
 cudaError_t forward_as(cudaStream_t st, const AttnArgs& a) {
   CUtensorMap q, k, v;
   const int64_t wq = (int64_t)a.H * D, wk = (int64_t)a.Hkv * D;
-  if (!make_map(&q, a.Q, a.T, wq, a.ldq) || !make_map(&k, a.K, a.T, wk, a.ldk) ||
-      !make_map(&v, a.V, a.T, wk, a.ldv))
-    return cudaErrorInvalidValue;
-  auto fn = k_attn_fwd_tc<D>;
-  const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)Cfg<D>::SMEM);
+  const SplitSrc src[3] = {{a.Q, a.ldq, wq}, {a.K, a.ldk, wk}, {a.V, a.ldv, wk}};
+  CUtensorMap* maps[3] = {&q, &k, &v};
+  cudaError_t err = make_maps<NP>(st, a, src, maps, 3);
+  if (err != cudaSuccess) return err;
+  auto fn = k_attn_fwd_tc<D, NP>;
+  constexpr size_t smem = Cfg<D, NP>::SMEM;
+  err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   const dim3 grid((unsigned)a.H * (unsigned)a.n_seqs,
                   (unsigned)((a.max_len + 2 * BM - 1) / (2 * BM)));
-  fn<<<grid, THREADS, Cfg<D>::SMEM, st>>>(q, k, v, a);
+  fn<<<grid, THREADS, smem, st>>>(q, k, v, a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_attn_fwd_tc(cudaStream_t st, const AttnArgs& a) {
-  return a.head_dim == 64 ? forward_as<64>(st, a) : forward_as<128>(st, a);
+  if (a.dtype == DUST_F32) return forward_as<64, 3>(st, a);
+  return a.head_dim == 64 ? forward_as<64, 1>(st, a) : forward_as<128, 1>(st, a);
 }
 
 }  // namespace dust

@@ -170,6 +170,36 @@ unsigned grid_for(int64_t n) {
   return (unsigned)(blocks < 1 ? 1 : (blocks > 2368 ? 2368 : blocks));
 }
 
+
+struct SplitArgs {
+  SplitSrc src[4];
+  int64_t T;
+  __nv_bfloat16* dst[4];
+};
+
+// Four values a thread: 16 bytes read, 3 x 8 written; bound by HBM.
+__global__ __launch_bounds__(256) void k_split_planes(SplitArgs a) {
+  const SplitSrc s = a.src[blockIdx.y];
+  const int64_t w4 = s.width / 4, n = a.T * w4;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / w4, col = (i - row * w4) * 4;
+    const float4 v = __ldcs(reinterpret_cast<const float4*>((const float*)s.p + row * s.ld + col));
+    float x[4] = {v.x, v.y, v.z, v.w};
+    __nv_bfloat16* out = a.dst[blockIdx.y] + row * 3 * s.width + col;
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      uint32_t h[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        h[e] = __float_as_uint(x[e]) & 0xffff0000u;  // truncated: exact to take off
+        x[e] -= __uint_as_float(h[e]);
+      }
+      *reinterpret_cast<uint2*>(out + p * s.width) =
+          make_uint2((h[0] >> 16) | h[1], (h[2] >> 16) | h[3]);
+    }
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_absmax_bf16(cudaStream_t st, const __nv_bfloat16* x, int64_t n,
@@ -200,6 +230,23 @@ cudaError_t launch_transpose_bf16(cudaStream_t st, const __nv_bfloat16* src, int
 cudaError_t launch_permute_rows_bf16(cudaStream_t st, const __nv_bfloat16* src, int64_t rows,
                                      int64_t cols, int64_t mul, __nv_bfloat16* dst) {
   k_permute_rows_bf16<<<(unsigned)rows, 128, 0, st>>>(src, rows, cols, mul, dst);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_split_planes(cudaStream_t st, const SplitSrc* src, int n, int64_t T,
+                                void* planes) {
+  SplitArgs a{};
+  a.T = T;
+  __nv_bfloat16* at = (__nv_bfloat16*)planes;
+  int64_t most = 0;
+  for (int i = 0; i < n; ++i) {
+    a.src[i] = src[i];
+    a.dst[i] = at;
+    at += T * 3 * src[i].width;
+    most = src[i].width > most ? src[i].width : most;
+  }
+  const int64_t blocks = (T * (most / 4) + 255) / 256;
+  k_split_planes<<<dim3((unsigned)(blocks < 4096 ? blocks : 4096), (unsigned)n), 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 
