@@ -17,6 +17,11 @@
 // sum l is taken over the unrounded P; rounding P to bf16 for the product (half
 // a step, 2^-8 relative, per term) is what puts it on the tensor cores.
 //
+// fp32 tensors: a CTA owns one query tile with two S buffers instead, which leaves
+// TMEM for the third plane of P and a total. The tensor cores truncate as they
+// add, so a tile's P V starts from zero and the softmax threads add it to the
+// total in fp32, rounded (1.9e-6 off over a sequence of 1024 without that).
+//
 // Warp roles: warp 0 TMA producer, warp 1 issues S products, warp 2 the PV
 // products, warps 4..7 and 8..11 are the softmax of either query tile. Rows past
 // a sequence's end and bounded waits as in k_attn_bwd_tc.cu.
@@ -30,15 +35,18 @@ constexpr float kGrow = 8.0f;  // log2 growth of a row's maximum that rescales O
 
 template <int D, int NP>
 struct Cfg {
+  static constexpr int G = NP == 3 ? 1 : 2;  // query tiles
   // key and value stages
-  static constexpr int STK = NP == 3 ? 1 : (D == 64 ? 4 : 3), STV = NP == 3 ? 1 : (D == 64 ? 4 : 2);
+  static constexpr int STK = NP == 3 ? 2 : (D == 64 ? 4 : 3), STV = NP == 3 ? 1 : (D == 64 ? 4 : 2);
   static constexpr int BOXES = D / 64;
   static constexpr int TILE_BYTES = NP * BM * D * 2;
-  static constexpr int K0 = 2 * TILE_BYTES, V0 = K0 + STK * TILE_BYTES;
+  static constexpr int K0 = G * TILE_BYTES, V0 = K0 + STK * TILE_BYTES;
   static constexpr int BARS = V0 + STV * TILE_BYTES;
   static constexpr size_t SMEM = 1024 + (size_t)BARS + 256;
-  static constexpr int O = 2 * BN, P2 = O + 2 * D;  // TMEM: S_0, S_1, O_0, O_1, third planes of P
-  static_assert(P2 + (NP == 3 ? 128 : 0) <= 512, "TMEM columns");
+  // TMEM: two S (of two query tiles, or of one in turn), O of each; NP 3: the total
+  // and P's third plane
+  static constexpr int O = 2 * BN, TOTAL = O + D, P2 = TOTAL + D;
+  static_assert(NP == 3 ? P2 + 64 <= 512 : O + 2 * D <= 512, "TMEM columns");
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -56,7 +64,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
     const __grid_constant__ CUtensorMap tmV, AttnArgs a) {
   using C = Cfg<D, NP>;
   using E = Elem<NP>;
-  constexpr int STK = C::STK, STV = C::STV;
+  constexpr int STK = C::STK, STV = C::STV, G = C::G;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -74,10 +82,10 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
     return;
   }
   const int len = (int)(end - beg);
-  const int r_first = 2 * tile * BM;
+  const int r_first = G * tile * BM;
   if (r_first >= len) return;
   // key tiles up to the diagonal; the second query tile may lie past the end
-  const int n0 = 2 * tile + 1, n1 = r_first + BM < len ? 2 * tile + 2 : 0;
+  const int n0 = G * tile + 1, n1 = G == 2 && r_first + BM < len ? 2 * tile + 2 : 0;
   const int n = max(n0, n1);
 
   if (threadIdx.x == 0) {
@@ -183,15 +191,18 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
       bool issued = false, ok = true;
       for (int j = 0; j < n && ok; ++j) {
         ok = wait(sh->kfull[j % STK], j / STK);
-        for (int g = 0; g < 2 && ok; ++g) {
+        for (int g = 0; g < G && ok; ++g) {
           if (j >= (g ? n1 : n0)) continue;
-          // P of the previous tile lies over S: its product is complete
-          ok = j == 0 ? wait(sh->res[g], 0) : wait(sh->odone[g], j - 1);
+          // P of the buffer's previous tile lies over S: its product is complete
+          const int b = G == 2 ? g : j & 1;
+          if (j == 0) ok = wait(sh->res[g], 0);
+          if (G == 2 && j > 0) ok = wait(sh->odone[g], j - 1);
+          if (G == 1 && j > 1) ok = wait(sh->odone[b], (j >> 1) - 1);
           if (!ok) break;
           ptx::tc_fence_after();
-          mma_scores<D, NP>(tmem + g * BN, base + g * C::TILE_BYTES,
+          mma_scores<D, NP>(tmem + b * BN, base + g * C::TILE_BYTES,
                             base + C::K0 + (j % STK) * C::TILE_BYTES);
-          ptx::mma_commit(ptx::smem_u32(&sh->sfull[g]));
+          ptx::mma_commit(ptx::smem_u32(&sh->sfull[b]));
           issued = true;
         }
         if (ok) ptx::mma_commit(ptx::smem_u32(&sh->kempty[j % STK]));
@@ -208,14 +219,15 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
       bool ok = true;
       for (int j = 0; j < n && ok; ++j) {
         ok = wait(sh->vfull[j % STV], j / STV);
-        for (int g = 0; g < 2 && ok; ++g) {
+        for (int g = 0; g < G && ok; ++g) {
           if (j >= (g ? n1 : n0)) continue;
           ok = wait(sh->pfull[g], j);
           if (!ok) break;
           ptx::tc_fence_after();
-          mma_sum<D, NP>(tmem + C::O + g * D, tmem + g * BN, tmem + C::P2 + 64 * g,
-                         base + C::V0 + (j % STV) * C::TILE_BYTES, j == 0);
-          ptx::mma_commit(ptx::smem_u32(&sh->odone[g]));
+          const int b = G == 2 ? g : j & 1;
+          mma_sum<D, NP>(tmem + C::O + g * D, tmem + b * BN, tmem + C::P2,
+                         base + C::V0 + (j % STV) * C::TILE_BYTES, NP == 3 || j == 0);
+          ptx::mma_commit(ptx::smem_u32(&sh->odone[b]));
         }
         if (ok) ptx::mma_commit(ptx::smem_u32(&sh->vempty[j % STV]));
       }
@@ -223,7 +235,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
       ptx::mma_commit(ptx::smem_u32(&sh->pvdone));
       wait_bounded(ptx::smem_u32(&sh->pvdone), 0, &dummy, a.status);
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 4 + 4 * G) {
     // ---------------- softmax ----------------
     const int g = (warp - 4) >> 2, quad = warp & 3;
     const int row = quad * 32 + lane;                  // TMEM lane
@@ -231,12 +243,39 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
     const int ng = g ? n1 : n0;
     const bool in = rr < len;
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-    const uint32_t ts = lane_base + g * BN, to = lane_base + C::O + g * D;
+    const uint32_t to = lane_base + C::O + g * D, total = lane_base + C::TOTAL;
     const float c2 = a.scale * kLog2e;
     float m = 0.0f, l = 0.0f;
     bool ok = true;
+    // the product of tile j is complete
+    auto done = [&](int j) {
+      ok = wait_warp(ptx::smem_u32(&sh->odone[G == 2 ? g : j & 1]),
+                     (uint32_t)(G == 2 ? j : j >> 1) & 1u, abort, a.status);
+      ptx::tc_fence_after();
+      return ok;
+    };
+    // NP 3: total = (total + the product of tile j) f
+    auto flush = [&](int j, float f) {
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t x[32], y[32], w[16];
+        ptx::tmem_ld32x2(to + 32 * c, x, total + 32 * c, y);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float o = __uint_as_float(x[16 * b + i]);
+            w[i] = __float_as_uint((j == 0 ? o : o + __uint_as_float(y[16 * b + i])) * f);
+          }
+          ptx::tmem_st16(total + 32 * c + 16 * b, w);
+        }
+      }
+    };
     for (int j = 0; j < ng; ++j) {
-      ok = wait_warp(ptx::smem_u32(&sh->sfull[g]), (uint32_t)j & 1u, abort, a.status);
+      const int sb = G == 2 ? g : j & 1;
+      const uint32_t ts = lane_base + sb * BN;
+      ok = wait_warp(ptx::smem_u32(&sh->sfull[sb]), (uint32_t)(G == 2 ? j : j >> 1) & 1u, abort,
+                     a.status);
       if (!ok) break;
       ptx::tc_fence_after();
       const bool diag = j == ng - 1;
@@ -260,11 +299,21 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
       if (j == 0) {
         m = top;
+      } else if (NP == 3) {
+        // (P's third plane has one buffer, so this tile's waits for the product anyway)
+        if (!done(j - 1)) break;
+        float f = 1.0f;
+        if (__any_sync(0xffffffffu, top > m + kGrow)) {
+          const float mn = fmaxf(m, top);
+          f = ex2(m - mn);
+          m = mn;
+          l *= f;
+        }
+        flush(j - 1, f);
+        // (the first half's registers are needed again: the loads below)
+        load(0);
       } else if (__any_sync(0xffffffffu, top > m + kGrow)) {
-        // O holds the tiles before this one
-        ok = wait_warp(ptx::smem_u32(&sh->odone[g]), (uint32_t)(j - 1) & 1u, abort, a.status);
-        if (!ok) break;
-        ptx::tc_fence_after();
+        if (!done(j - 1)) break;  // O holds the tiles before this one
         const float mn = fmaxf(m, top), f = ex2(m - mn);
         m = mn;
         l *= f;
@@ -296,7 +345,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
             sum[i & 1] = __fadd2_rn(sum[i & 1], v[i]);
           }
           // P's columns lie over those of S that this thread has read
-          store_planes<NP>(ts + 64 * h + 16 * b, lane_base + C::P2 + 64 * g + 32 * h + 16 * b, v);
+          store_planes<NP>(ts + 64 * h + 16 * b, lane_base + C::P2 + 32 * h + 16 * b, v);
         }
       }
       l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
@@ -305,13 +354,14 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh->pfull[g]));
     }
-    if (ok && ng > 0)
-      ok = wait_warp(ptx::smem_u32(&sh->odone[g]), (uint32_t)(ng - 1) & 1u, abort, a.status);
-    if (ok && ng > 0 && !*abort) {
-      ptx::tc_fence_after();
+    if (ok && ng > 0 && done(ng - 1) && !*abort) {
+      if (NP == 3) {
+        flush(ng - 1, 1.0f);
+        ptx::tmem_wait_st();
+      }
       const int64_t r = beg + rr;
       if (in) a.lse_out[r * a.H + head] = 0.6931471805599453f * m + logf(l);
-      store_row<D / 32>(to, 1.0f / l, (E*)a.O + r * a.ldo + (int64_t)head * D, in);
+      store_row<D / 32>(NP == 3 ? total : to, 1.0f / l, (E*)a.O + r * a.ldo + (int64_t)head * D, in);
     }
   }
 
@@ -334,7 +384,7 @@ cudaError_t forward_as(cudaStream_t st, const AttnArgs& a) {
   err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   const dim3 grid((unsigned)a.H * (unsigned)a.n_seqs,
-                  (unsigned)((a.max_len + 2 * BM - 1) / (2 * BM)));
+                  (unsigned)((a.max_len + Cfg<D, NP>::G * BM - 1) / (Cfg<D, NP>::G * BM)));
   fn<<<grid, THREADS, smem, st>>>(q, k, v, a);
   return cudaGetLastError();
 }
