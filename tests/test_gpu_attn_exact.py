@@ -273,3 +273,76 @@ def test_the_estimator_converges_to_the_exact_gradient(ctx):
         cos = torch.nn.functional.cosine_similarity(g.flatten().double(),
                                                     ex[name].flatten().double(), dim=0)
         assert float(cos) > 0.99, which
+
+
+def test_cosine_against_the_exact_gradient_follows_the_law(ctx):
+    # for a linear response and n Gaussian channels cos(K) = 1 / sqrt(1 + (n + 1) / K)
+    # per token; value noise is exactly linear, so its curve is the law's within
+    # the sampling noise of 96 tokens x 64 channels
+    from zeroth_order_transformer_dust_b200.alignment import attn_cosine_vs_k
+    T, L, dh = 96, 48, 64
+    q, k, v, e = _inputs(T, 1, 1, dh, "f32", 22)
+    x = torch.randn(T, 16, device="cuda")
+    for which in ("q", "k", "v"):
+        res = attn_cosine_vs_k(ctx, x, q, k, v, e, seq_len=L, n_heads=1, which=which,
+                               ks=[64, 512, 4096], sigma=1e-3)
+        assert res["K"] == [64, 512, 4096] and res["cos_g"] == sorted(res["cos_g"])
+        assert res["cos_g"][-1] > 0.97
+        if which == "v":
+            for K, c in zip(res["K"], res["cos_g"]):
+                assert abs(c - (1 + (dh + 1) / K) ** -0.5) < 0.03
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dh", [64, 128])
+def test_cuda_core_form(monkeypatch, dtype, dh):
+    # what a context without tensor cores runs, at widths they otherwise take
+    monkeypatch.setenv("DUST_DISABLE_TC", "1")
+    c = dust.Context(0)
+    _check(c, [130, 1, 64], 4, 2, dh, dtype, fused=True, first=3, tail=9)
+    c.close()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_growing_scores_move_the_maximum(ctx, dtype):
+    # keys that grow along the sequence: the running maximum moves by far more
+    # than the rescaling threshold in every tile, and shrinking ones never move it
+    T, heads, dh = 520, 2, 64
+    q, k, v, e = _inputs(T, heads, heads, dh, dtype, 4)
+    ramp = torch.linspace(0.1, 6.0, T, device="cuda")[:, None]
+    for r in (ramp, ramp.flip(0)):
+        kk = (k.float() * r).to(k.dtype)
+        f = ctx.attn_forward(q, kk, v, n_heads=heads)
+        g = ctx.attn_backward(q, kk, v, f["O"], f["lse"], e, n_heads=heads)
+        ref = oracle.exact_attention(np64(q), np64(kk), np64(v), [0, T], heads, heads, E=np64(e))
+        z, rnd = _sizes(q, kk, v, e, f["O"], [0, T], heads, heads, dh ** -0.5)
+        # scores reach ~100: exponents carry |s| 2^-23 more than F32 covers
+        slack = 100 * 2.0 ** -22
+        for name, x in {**f, **g}.items():
+            if name == "lse":
+                assert np.all(np.abs(np64(x) - ref["lse"]) <= 5e-5 * (1 + np.abs(ref["lse"])))
+                continue
+            tol = (F32 + slack) * z[name] + HALF[dtype] * (rnd[name] + np.abs(ref[name])) + 1e-30
+            assert np.all(np.abs(np64(x) - ref[name]) <= tol), name
+
+
+def test_offsets_past_32_bits(ctx):
+    # two sequences whose rows lie more than 2^31 elements into their tensors
+    ld, T, dh = 1 << 20, 2200, 64
+    buf = torch.zeros(T * ld, dtype=torch.bfloat16, device="cuda").view(T, ld)
+    gen = torch.Generator().manual_seed(2)
+    x = torch.randn(150, 4 * dh, generator=gen).to(torch.bfloat16).cuda()
+    buf[2050:, :4 * dh] = x
+    cu = torch.tensor([2050, 2180, 2200], dtype=torch.int32, device="cuda")
+    kw = dict(n_heads=1, cu_seqlens=cu, max_len=130)
+    part = lambda t: t.split(dh, 1)  # noqa: E731
+    q, k, v, e = part(buf[:, :4 * dh])
+    f = ctx.attn_forward(q, k, v, out={"O": buf[:, 4 * dh:5 * dh]}, **kw)
+    g = ctx.attn_backward(q, k, v, f["O"], f["lse"], e, **kw)
+    q, k, v, e = (t.contiguous() for t in part(x))
+    kw["cu_seqlens"] = cu - 2050
+    f2 = ctx.attn_forward(q, k, v, **kw)
+    g2 = ctx.attn_backward(q, k, v, f2["O"], f2["lse"], e, **kw)
+    assert torch.equal(f["O"][2050:], f2["O"]) and torch.equal(f["lse"][2050:], f2["lse"])
+    for n in g2:
+        assert torch.equal(g[n][2050:], g2[n]), n

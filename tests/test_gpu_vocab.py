@@ -352,3 +352,41 @@ def test_vocab_calls_in_a_graph_and_on_another_stream(ctx):
             assert torch.equal(want[name], static[name]), name
     ctx.check()
     other.close()
+
+
+def test_vocab_offsets_past_32_bits(ctx):
+    # the last rows lie more than 2^31 elements into the logits
+    T, V, k = 17000, 128256, 5
+    Z = torch.zeros(T, V, dtype=torch.bfloat16, device="cuda")
+    last = _logits(6, V, "bf16", seed=4)
+    Z[-6:] = last
+    ids, vals = _teacher(6, V, k, 4, missing=False)
+    di = torch.full((T, k), -1, dtype=torch.int32, device="cuda")
+    dv = torch.zeros(T, k, device="cuda")
+    di[-6:], dv[-6:] = _dev(ids, vals)[:2]
+    got = ctx.token_logprobs(Z, torch.zeros(T, dtype=torch.int32, device="cuda"), top=3)
+    want = ctx.token_logprobs(last, torch.zeros(6, dtype=torch.int32, device="cuda"), top=3)
+    assert torch.equal(got["top_ids"][-6:], want["top_ids"])
+    torch.testing.assert_close(got["logp"][-6:], want["logp"], rtol=1e-5, atol=1e-5)
+    assert got["top_ids"][0].tolist() == [0, 1, 2]
+    ref = ctx.distill(last, di[-6:].contiguous(), dv[-6:].contiguous())
+    got = ctx.distill(Z, di, dv, out={"dZ": Z})
+    # one CTA a row here and a cluster there: the row's sum in another order
+    torch.testing.assert_close(got["loss"][-6:], ref["loss"], rtol=1e-5, atol=1e-5)
+    torch.testing.assert_close(Z[-6:].float(), ref["dZ"].float(), rtol=2.0 ** -7, atol=1e-9)
+    assert not got["loss"][:-6].any() and not Z[:64].any()
+
+
+@pytest.mark.parametrize("every", [2, 3, 10])
+def test_distill_with_periodic_padding(ctx, every):
+    # more rows than resident CTAs, a mask of every n-th and of the first 700
+    T, V, k = 1500, 2003, 4
+    Z = _logits(T, V, "bf16", seed=every)
+    ids, vals = _teacher(T, V, k, every)
+    w = np.ones(T, dtype=np.float32)
+    w[::every] = 0.0
+    w[:700] = 0.0
+    di, dv, dw = _dev(ids, vals, w)
+    got = ctx.distill(Z, di, dv, weights=dw)
+    _check_distill(got, Z, ids, vals, 1.0, w, "bf16")
+    assert not got["dZ"][:700].any() and not got["loss"][:700].any()

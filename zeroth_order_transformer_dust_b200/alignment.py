@@ -1,4 +1,4 @@
-"""Gradient alignment of the LM-head estimator against the exact gradient.
+"""Gradient alignment of the LM-head and attention estimators against the exact gradients.
 
 The pages ("Dust：无需反向传播的Transformer零阶预训练", §2 梯度对齐) report that
 the cosine between the estimate and the true gradient follows
@@ -98,4 +98,37 @@ def cosine_vs_k(ctx, H, W, y, *, ks, sigma, S=0, seed=0, token_chunk=2048):
             G_est.flatten().double(), G_true.flatten().double(), dim=0)))
     res["fit_g"] = fit_cos_law(res["K"], res["cos_g"])
     res["fit_G"] = fit_cos_law(res["K"], res["cos_G"])
+    return res
+
+
+@torch.no_grad()
+def attn_cosine_vs_k(ctx, X, Q, K_cache, V_cache, E, *, seq_len, n_heads, which, ks, sigma,
+                     seed=0):
+    """The same curve for the attention-internals estimator: cosine of g (T x D)
+    and G (D x d) of the query ("q"), key ("k") or value ("v") projection with
+    the exact gradients, which ``attn_forward`` and ``attn_backward`` give."""
+    ks = sorted(int(k) for k in ks)
+    shape = dict(n_heads=n_heads, seq_len=seq_len)
+    f = ctx.attn_forward(Q, K_cache, V_cache, **shape)
+    exact = ctx.attn_backward(Q, K_cache, V_cache, f["O"], f["lse"], E, **shape)
+    g_true = exact["d" + which.upper()].double()
+    G_true = g_true.t() @ X.double()
+
+    def cosine(a, b):
+        return float((a * b).sum() / torch.sqrt((a * a).sum() * (b * b).sum()).clamp_min(1e-300))
+
+    acc = torch.zeros_like(Q)
+    blk = torch.empty_like(Q)
+    res = {"K": [], "cos_g": [], "cos_G": []}
+    done = 0
+    for k in ks:
+        ctx.attn_grad(X, Q, K_cache, V_cache, E, which=which, K=k - done, sigma=sigma, seed=seed,
+                      draw_offset=done, want_G=False, out={"g": blk}, **shape)
+        acc.add_(blk, alpha=float(k - done))
+        done = k
+        g = acc.double() / k
+        res["K"].append(k)
+        res["cos_g"].append(cosine(g, g_true))
+        res["cos_G"].append(cosine(g.t() @ X.double(), G_true))
+    res["fit_g"] = fit_cos_law(res["K"], res["cos_g"])
     return res

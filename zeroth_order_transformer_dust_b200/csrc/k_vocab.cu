@@ -606,16 +606,17 @@ __global__ __launch_bounds__(MODE == kLossOnly ? kLpThreads
   const int rank = ranks > 1 ? (int)ptx::cluster_ctarank() : 0;
   // the k-th row of this cluster: one of every `step` rows, moved on by 7 from one
   // to the next, so that a periodic mask does not leave some clusters all its rows
-  const int64_t step = gridDim.x / ranks, first = blockIdx.x / ranks;
-  auto row_of = [&](int64_t k) { return k * step + (first + 7 * k) % step; };
+  // (T <= 2^27: 32 bits do)
+  const int T = (int)a.T, step = (int)gridDim.x / ranks, first = (int)blockIdx.x / ranks;
+  auto row_of = [&](int k) { return k * step + (first + 7 * k) % step; };
   // this thread's teacher entry of a row: absent (-1) where its id is -1 or its
   // value -inf
   int32_t id = -1;
   float v = -inf_f(), weight = 1.0f;
   // (loaded without a condition, so that nothing waits for the values here)
-  auto entry = [&](int64_t t) {
-    if (t >= a.T) t = a.T - 1;
-    const int64_t e = t * a.k + min(tid, a.k - 1);
+  auto entry = [&](int t) {
+    if (t >= T) t = T - 1;
+    const int64_t e = (int64_t)t * a.k + min(tid, a.k - 1);
     id = a.ids[e];
     v = a.vals[e];
     weight = *(a.weights ? a.weights + t : &kOne);
@@ -623,10 +624,10 @@ __global__ __launch_bounds__(MODE == kLossOnly ? kLpThreads
   // From the k-th row on, whose entry is loaded, the first that is not left out
   // (its row T or past it: none). A row without a teacher entry, or of weight 0,
   // gets zeros and its logits are not read. All CTAs of a cluster see the same rows.
-  auto next_live = [&](int64_t& k) {
-    for (; k * step < a.T; entry(row_of(++k))) {
-      const int64_t t = row_of(k);
-      if (t >= a.T) continue;  // (in the last, incomplete round)
+  auto next_live = [&](int& k) {
+    for (; k * step < T; entry(row_of(++k))) {
+      const int t = row_of(k);
+      if (t >= T) continue;  // (in the last, incomplete round)
       if (tid >= a.k) id = -1;
       if (id != -1 && (id < 0 || (int64_t)id >= a.V)) {
         atomicOr(a.status, kStatusBadTarget);
@@ -638,8 +639,8 @@ __global__ __launch_bounds__(MODE == kLossOnly ? kLpThreads
       }
       if (sync_threads_or(id >= 0, THREADS) && weight != 0.0f) return t;
       if (MODE != kLossOnly) {
-        const Slice sl = slice_of(Z + t * a.ld, a.V, rank, ranks);
-        E* out = dZ + t * a.ldg;
+        const Slice sl = slice_of(Z + (int64_t)t * a.ld, a.V, rank, ranks);
+        E* out = dZ + (int64_t)t * a.ldg;
         const int c0 = rank == 0 ? 0 : sl.head + sl.v0 * N;
         const int c1 = rank == ranks - 1 ? (int)a.V : sl.head + sl.v1 * N;
         const int lead = (int)((16 - ((uintptr_t)(out + c0) & 15)) & 15) / (int)sizeof(E);
@@ -651,7 +652,7 @@ __global__ __launch_bounds__(MODE == kLossOnly ? kLpThreads
       }
       if (rank == 0 && tid == 0 && a.loss) a.loss[t] = 0.0f;
     }
-    return a.T;
+    return T;
   };
   // chunks of the longest slice of any row
   const int chunks = MODE == kResident
@@ -670,16 +671,16 @@ __global__ __launch_bounds__(MODE == kLossOnly ? kLpThreads
     if (tid >= THREADS) {
       // ---------------- the copies ----------------
       int rows = 0;
-      for (int64_t k = 0; k * step < a.T; ++k) {
-        const int64_t t = row_of(k);
-        if (t >= a.T) continue;
+      for (int k = 0; k * step < T; ++k) {
+        const int t = row_of(k);
+        if (t >= T) continue;
         bool any = false;
         for (int j = lane; j < a.k; j += 32) {
-          const int32_t e = a.ids[t * a.k + j];
-          any |= e >= 0 && (int64_t)e < a.V && a.vals[t * a.k + j] != -inf_f();
+          const int32_t e = a.ids[(int64_t)t * a.k + j];
+          any |= e >= 0 && (int64_t)e < a.V && a.vals[(int64_t)t * a.k + j] != -inf_f();
         }
         if (!__any_sync(0xffffffffu, any) || (a.weights && a.weights[t] == 0.0f)) continue;
-        const E* row = Z + t * a.ld;
+        const E* row = Z + (int64_t)t * a.ld;
         const Slice sl = slice_of(row, a.V, rank, ranks);
         const int bytes = (sl.v1 - sl.v0) * 16;
         const uint8_t* src = reinterpret_cast<const uint8_t*>(row + sl.head) + (int64_t)sl.v0 * 16;
@@ -708,13 +709,13 @@ __global__ __launch_bounds__(MODE == kLossOnly ? kLpThreads
   // the row is overwritten (dZ may be Z)
   float z_next = 0.0f;
   auto gather = [&](const E* row) { z_next = load_rw(row + max(id, 0)); };
-  int64_t k = 0;
+  int k = 0;
   entry(row_of(k));
-  int64_t t = next_live(k);
-  if (t < a.T) gather(Z + t * a.ld);
-  for (uint32_t par = 0; t < a.T; par ^= 1u) {
-    const E* row = Z + t * a.ld;
-    E* out = MODE == kLossOnly ? nullptr : dZ + t * a.ldg;
+  int t = next_live(k);
+  if (t < T) gather(Z + (int64_t)t * a.ld);
+  for (uint32_t par = 0; t < T; par ^= 1u) {
+    const E* row = Z + (int64_t)t * a.ld;
+    E* out = MODE == kLossOnly ? nullptr : dZ + (int64_t)t * a.ldg;
     const Slice sl = slice_of(row, a.V, rank, ranks);
     const uint4* body = reinterpret_cast<const uint4*>(row + sl.head);
     const int nv = sl.v1 - sl.v0;
@@ -837,8 +838,8 @@ __global__ __launch_bounds__(MODE == kLossOnly ? kLpThreads
       }
     }
     // the next row's entries, and zeros for the rows left out before it
-    const int64_t tn = next_live(++k);
-    gather(tn < a.T ? Z + tn * a.ld : row);
+    const int tn = next_live(++k);
+    gather(tn < T ? Z + (int64_t)tn * a.ld : row);
     if (MODE != kLossOnly) {
       auto grads = [&](const uint4& w) {
         float z[N];
