@@ -396,7 +396,9 @@ dust_status dust_attn_forward(dust_ctx* ctx, const dust_attn_dims* dims, const v
  *            a key/value head); dtype as the inputs, rounded once
  *   work     as above, dust_attn_work_bytes(dims, 1) bytes, not NULL
  * The probabilities are recomputed from lse; no sum uses atomics, so results
- * are the same from run to run. Outputs must not overlap the inputs.
+ * are the same from run to run. Outputs must not overlap the inputs or one
+ * another (the same address is refused; interleaved columns of one tensor are
+ * not an overlap).
  * Errors as dust_attn_forward. */
 dust_status dust_attn_backward(dust_ctx* ctx, const dust_attn_dims* dims, const void* Q,
                                const void* Kc, const void* Vc, const void* O, const float* lse,

@@ -254,8 +254,18 @@ def test_refusals(ctx):
         ctx.attn_backward(q, k, v, f["O"], f["lse"][:, :2], e, **ok)
     with pytest.raises(TypeError):
         ctx.attn_forward(q, k, v, cu_seqlens=torch.zeros(2, dtype=torch.int64, device="cuda"), **ok)
+    for out in ({"dQ": q}, {"dQ": e}, {"dK": k}, {"dV": k}):
+        with pytest.raises(dust.DustError, match="overlap"):
+            ctx.attn_backward(q, k, v, f["O"], f["lse"], e, out=out, **ok)
+    with pytest.raises(dust.DustError, match="overlap"):
+        ctx.attn_forward(q, k, v, out={"O": q}, **ok)
+    same = torch.empty_like(k)
+    with pytest.raises(dust.DustError, match="apart"):
+        ctx.attn_backward(q, k, v, f["O"], f["lse"], e, out={"dK": same, "dV": same}, **ok)
     empty = ctx.attn_forward(q[:0], k[:0], v[:0], **ok)
     assert empty["O"].shape == (0, 256)
+    assert ctx.attn_backward(q[:0], k[:0], v[:0], empty["O"], empty["lse"], e[:0],
+                             **ok)["dQ"].shape == (0, 256)
 
 
 def test_the_estimator_converges_to_the_exact_gradient(ctx):

@@ -6,6 +6,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 
 #include "internal.cuh"
 #include "noise.cuh"
@@ -363,6 +364,15 @@ dust_status check_rows(dust_ctx* ctx, const AttnArgs& a, const char* name, const
   if (a.T > 1 && (ld < width || ld > (1LL << 31)))
     return fail(ctx, DUST_ERR_ARG, "%s's row stride must lie in [%lld, 2^31]", name,
                 (long long)width);
+  return DUST_OK;
+}
+
+// The kernels read the inputs after they have begun to write the outputs.
+dust_status check_apart(dust_ctx* ctx, std::initializer_list<const void*> outputs,
+                        std::initializer_list<const void*> inputs) {
+  for (const void* o : outputs)
+    for (const void* i : inputs)
+      if (o && o == i) return fail(ctx, DUST_ERR_ARG, "outputs must not overlap the inputs");
   return DUST_OK;
 }
 
@@ -1153,6 +1163,7 @@ dust_status dust_attn_forward(dust_ctx* ctx, const dust_attn_dims* dims, const v
   DUST_TRY(check_rows(ctx, a, "V", Vc, a.ldv, dk));
   DUST_TRY(check_rows(ctx, a, "O", O_out, a.ldo, dq));
   if (a.T > 0 && !lse_out) return fail(ctx, DUST_ERR_ARG, "lse must be non-NULL");
+  DUST_TRY(check_apart(ctx, {O_out}, {Q, Kc, Vc}));
   if (!aligned(lse_out, 4) || !aligned(work, 256))
     return fail(ctx, DUST_ERR_ARG, "lse must be 4-byte and work 256-byte aligned");
   DUST_CU(cudaSetDevice(ctx->device));
@@ -1185,6 +1196,9 @@ dust_status dust_attn_backward(dust_ctx* ctx, const dust_attn_dims* dims, const 
   DUST_TRY(check_rows(ctx, a, "dQ", dQ_out, a.lddq, dq));
   DUST_TRY(check_rows(ctx, a, "dK", dK_out, a.lddk, dk));
   DUST_TRY(check_rows(ctx, a, "dV", dV_out, a.lddv, dk));
+  DUST_TRY(check_apart(ctx, {dQ_out, dK_out, dV_out}, {Q, Kc, Vc, O, E}));
+  if (a.T > 0 && (dQ_out == dK_out || dQ_out == dV_out || dK_out == dV_out))
+    return fail(ctx, DUST_ERR_ARG, "dQ, dK and dV must be apart from one another");
   if (a.T > 0 && (!lse || !work)) return fail(ctx, DUST_ERR_ARG, "lse and work must be non-NULL");
   if (!aligned(lse, 4) || !aligned(work, 256))
     return fail(ctx, DUST_ERR_ARG, "lse must be 4-byte and work 256-byte aligned");

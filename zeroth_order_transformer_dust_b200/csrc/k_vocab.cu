@@ -235,7 +235,12 @@ __device__ __forceinline__ Stat stat_cluster(const Stat& a, float k2, Stat* mine
 // past its limit it is sorted, cut to n, and the threshold moves to the n-th.
 // The first threshold is the n-th largest of the threads' maxima over the
 // first tiles (n elements at least are not below it), so on ordinary rows about
-// n (1 + ln(V / tile)) elements ever enter. Any row is handled: a tile that
+// n (1 + ln(V / tile)) elements ever enter. Cutting at 2 n entries and not at 512
+// took 4096 x 128256 fp32 with n = 64 from 790 to 467 us together with the
+// cheaper ordering; without alternatives the same logits take 316 us (6.7 TB/s,
+// the copy rate). 8192 x 50257 bf16: 150 us, 5.5 TB/s. 4 x 128256 fp32 with n =
+// 20, eight CTAs a row: 13 us, 7 of them for the statistics alone. Any row is
+// handled: a tile that
 // enters whole fits the list. List order depends on timing, the sorted list
 // does not: keys are (value, ~index), all different.
 constexpr int kLpThreads = 256;
@@ -544,9 +549,15 @@ __global__ __launch_bounds__(kLpThreads, TOP || sizeof(E) == 2 ? 4 : 3) void k_t
 // a chunk's gradient is written the same chunk of the next row is copied in, so
 // reads and writes overlap within the CTA; two CTAs share an SM. Rows past 8
 // buffers (kReread) are read from global memory twice. The loss alone is a
-// streaming pass. The copies are a warp's own (warp 15): refilled by one of the
-// computing threads, who then waits for the others chunk by chunk, the same
-// scheme took 583 us where this one takes @@ (8192 x 50304 bf16).
+// streaming pass.
+//
+// Measured: 8192 x 50304 bf16 (a tenth of the rows left out) 358 us, 4.4 TB/s;
+// 2048 x 128256 fp32 417 us, 4.8 TB/s; the loss of 1000 x 50304 fp32 37 us, 5.4
+// TB/s. The gradient takes two exponentials per logit, and without them the same
+// copies and stores take 266 and 375 us: what is left is the exponentials' issue
+// slots, not the memory. The copies are a warp's own: refilled by one of the
+// computing threads, which then waits for the others chunk by chunk, the first
+// case took 583 us.
 enum DistillMode { kLossOnly = 0, kResident = 1, kReread = 2 };
 constexpr int kDsThreads = 480;             // (loss alone: kLpThreads, for more rows at a time)
 constexpr int kMaxTeacher = kTopLimit;
