@@ -297,6 +297,16 @@ def test_distill_refusals(ctx):
     assert e.value.status == 4
     ids[2, 1] = -1
     _check_distill({"dZ": out["dZ"]}, Z, ids, vals, 1.0, None, "f32")
+    # far outside, in every entry of the last rows: no live row follows
+    di[2:] = 1 << 30
+    di[3, 0] = -(1 << 30)
+    ids[2:] = -1
+    for rows in (Z, _logits(4, 60000, "f32")):
+        out = {"dZ": torch.empty_like(rows)}
+        with pytest.raises(dust.DustError) as e:
+            ctx.distill(rows, di, dv, out=out)
+        assert e.value.status == 4
+        assert not out["dZ"][2:].any() and out["dZ"][0].any()
 
 
 def test_teacher_scores_feed_the_student(ctx):

@@ -257,6 +257,8 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
     """Elements between the rows of a 2-D tensor whose rows are contiguous
     and do not overlap."""
     shape = t.shape
+    if len(shape) == 2 and t.is_contiguous():
+        return shape[1]
     if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D, got shape {tuple(shape)}")
     rows, width = shape
@@ -323,14 +325,15 @@ def _exact_attn_dims(Q, K_cache, V_cache, n_heads, n_kv_heads, seq_len, cu_seqle
     if n_kv_heads < 1 or n_heads % n_kv_heads:
         raise ValueError("n_heads must be a multiple of n_kv_heads")
     head_dim = D // n_heads
+    kv = (T, n_kv_heads * head_dim)
     for t, n in ((K_cache, "K_cache"), (V_cache, "V_cache")):
-        _shape(t, (T, n_kv_heads * head_dim), n)
+        if t.shape != kv:
+            _shape(t, kv, n)
         if t.dtype != Q.dtype:
             raise TypeError(f"{n} must have Q's dtype")
-    dims = DustAttnDims(T=T, n_heads=n_heads, n_kv_heads=n_kv_heads, head_dim=head_dim,
-                        dtype=_dtype_code(Q), scale=0.0 if scale is None else scale,
-                        ldq=_row_stride(Q, "Q"), ldk=_row_stride(K_cache, "K_cache"),
-                        ldv=_row_stride(V_cache, "V_cache"))
+    dims = DustAttnDims(T, None, 0, 0, n_heads, n_kv_heads, head_dim, _dtype_code(Q),
+                        0.0 if scale is None else scale, 0, _row_stride(Q, "Q"),
+                        _row_stride(K_cache, "K_cache"), _row_stride(V_cache, "V_cache"))
     if scale is not None and not scale > 0.0:
         raise ValueError("scale must be > 0")
     if cu_seqlens is not None:
@@ -549,16 +552,17 @@ class Context:
 
     # -- exact losses and gradients ------------------------------------------------
     def _cuda(self, t: torch.Tensor, name: str):
-        if not t.is_cuda or t.device.index != self.device:
+        if t.get_device() != self.device:
             raise ValueError(f"{name} must be on cuda:{self.device}")
         return t
 
-    def _empty(self, shape, dtype, device) -> torch.Tensor:
-        """Memory for this context's stream (outputs and scratch of a call)."""
+    def _empty(self, shape, dtype, like) -> torch.Tensor:
+        """Memory for this context's stream (outputs and scratch of a call),
+        where ``like`` is."""
         if self._stream is None:
-            return torch.empty(shape, dtype=dtype, device=device)
+            return like.new_empty(shape, dtype=dtype)
         with torch.cuda.stream(self._stream):
-            return torch.empty(shape, dtype=dtype, device=device)
+            return like.new_empty(shape, dtype=dtype)
 
     def token_logprobs(self, Z, tokens=None, *, top=0, want_entropy=True, asynchronous=False,
                        out=None) -> dict:
@@ -585,7 +589,7 @@ class Context:
             if key in out:
                 _check_output(out, key, shape, dt, self.device)
             else:
-                out[key] = self._empty(shape, dt, Z.device)
+                out[key] = self._empty(shape, dt, Z)
             p[key] = out[key].data_ptr()
         self._bind_stream()
         self._check(self._L.dust_token_logprobs(self._h, T, V, _dtype_code(Z), Z.data_ptr(), ld,
@@ -615,14 +619,14 @@ class Context:
             if "loss" in out:
                 _check_output(out, "loss", (T,), torch.float32, self.device)
             else:
-                out["loss"] = self._empty((T,), torch.float32, Z.device)
+                out["loss"] = self._empty((T,), torch.float32, Z)
             loss = out["loss"]
         if want_grad:
             if "dZ" in out:
                 _check_output(out, "dZ", (T, V), Z.dtype, self.device, rows=True)
                 ldg = _row_stride(out["dZ"], "output dZ")
             else:
-                out["dZ"] = self._empty((T, ld), Z.dtype, Z.device)
+                out["dZ"] = self._empty((T, ld), Z.dtype, Z)
                 if ld != V:
                     out["dZ"] = out["dZ"][:, :V]
                 ldg = ld
@@ -652,7 +656,7 @@ class Context:
         if "lse" in out:
             _check_output(out, "lse", (dims.T, n_heads), torch.float32, self.device)
         else:
-            out["lse"] = self._empty((dims.T, n_heads), torch.float32, Q.device)
+            out["lse"] = self._empty((dims.T, n_heads), torch.float32, Q)
         self._attn_call(dims, cu_seqlens, asynchronous)
         work = self._attn_work(dims, 0, Q) if Q.dtype == torch.float32 else None
         self._check(self._L.dust_attn_forward(
@@ -696,7 +700,7 @@ class Context:
     def _rows_out(self, out: dict, key: str, like: torch.Tensor) -> int:
         """The row stride of an output like ``like``, made where it is not given."""
         if key not in out:
-            out[key] = self._empty(like.shape, like.dtype, like.device)
+            out[key] = self._empty(like.shape, like.dtype, like)
             return like.shape[1]
         _check_output(out, key, like.shape, like.dtype, self.device, rows=True)
         return _row_stride(out[key], f"output {key}")
@@ -704,7 +708,7 @@ class Context:
     def _attn_work(self, dims: DustAttnDims, backward: int, like: torch.Tensor) -> torch.Tensor:
         """Scratch of a call (from torch's allocator, so a captured graph has its own)."""
         n = self._L.dust_attn_work_bytes(ctypes.byref(dims), backward)
-        return self._empty((max(n, 0),), torch.uint8, like.device)  # (-1: the call refuses dims)
+        return self._empty((max(n, 0),), torch.uint8, like)  # (-1: the call refuses dims)
 
     def _attn_call(self, dims: DustAttnDims, cu_seqlens, asynchronous: bool):
         if cu_seqlens is not None:

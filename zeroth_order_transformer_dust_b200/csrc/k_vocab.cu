@@ -607,8 +607,8 @@ __device__ __forceinline__ void wait_phase(uint64_t& bar, uint32_t parity, uint3
 template <typename E, int MODE>
 __global__ __launch_bounds__(MODE == kLossOnly ? kLpThreads
                                                : kDsThreads + (MODE == kResident ? 32 : 0),
-                             MODE == kResident ? 2 : (MODE == kLossOnly ? 4 : 1)) void k_distill(const E* Z, E* dZ,
-                                                                       DistillArgs a, int ranks) {
+                             MODE == kResident ? 2 : (MODE == kLossOnly ? 4 : 1))
+    void k_distill(const E* Z, E* dZ, DistillArgs a, int ranks) {
   constexpr int N = Vec<E>::N;
   constexpr int THREADS = MODE == kLossOnly ? kLpThreads : kDsThreads;
   extern __shared__ __align__(128) uint8_t buf[];  // kResident: the slice's vectors
@@ -850,7 +850,7 @@ __global__ __launch_bounds__(MODE == kLossOnly ? kLpThreads
     }
     // the next row's entries, and zeros for the rows left out before it
     const int tn = next_live(++k);
-    gather(tn < T ? Z + (int64_t)tn * a.ld : row);
+    if (tn < T) gather(Z + (int64_t)tn * a.ld);  // (else the entry is not checked)
     if (MODE != kLossOnly) {
       auto grads = [&](const uint4& w) {
         float z[N];
