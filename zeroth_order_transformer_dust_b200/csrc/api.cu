@@ -1172,10 +1172,9 @@ dust_status dust_attn_forward(dust_ctx* ctx, const dust_attn_dims* dims, const v
   a.planes = attn_planes(a) ? work : nullptr;
   a.status = ctx->d_status;
   mark(ctx, nullptr);
-  DUST_CU(ctx->tc_enabled && attn_exact_tc_supported(a, false)
-              ? launch_attn_fwd_tc(ctx->stream, a)
-              : launch_attn_exact_simt(ctx->stream, a, false));
-  ctx->launches += a.planes ? 2 : 1;
+  const bool tc = ctx->tc_enabled && attn_exact_tc_supported(a, false);
+  DUST_CU(tc ? launch_attn_fwd_tc(ctx->stream, a) : launch_attn_exact_simt(ctx->stream, a, false));
+  ctx->launches += tc && a.planes ? 2 : 1;
   mark(ctx, "attn_forward");
   return finish(ctx, dims->flags);
 }
@@ -1209,10 +1208,9 @@ dust_status dust_attn_backward(dust_ctx* ctx, const dust_attn_dims* dims, const 
   a.planes = attn_planes(a) ? (char*)work + attn_delta_bytes(a) : nullptr;
   a.status = ctx->d_status;
   mark(ctx, nullptr);
-  DUST_CU(ctx->tc_enabled && attn_exact_tc_supported(a, true)
-              ? launch_attn_bwd_tc(ctx->stream, a)
-              : launch_attn_exact_simt(ctx->stream, a, true));
-  ctx->launches += a.planes ? 4 : 2;
+  const bool tc = ctx->tc_enabled && attn_exact_tc_supported(a, true);
+  DUST_CU(tc ? launch_attn_bwd_tc(ctx->stream, a) : launch_attn_exact_simt(ctx->stream, a, true));
+  ctx->launches += tc && a.planes ? 4 : 2;
   mark(ctx, "attn_backward");
   return finish(ctx, dims->flags);
 }
