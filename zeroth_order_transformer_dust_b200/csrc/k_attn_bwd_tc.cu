@@ -23,13 +23,14 @@
 //
 // Warp roles: warp 0 TMA producer, warp 1 issues the score products, warp 10 the
 // gradient products (one thread for both spends more time between its waits
-// than the tensor pipe does on the MMAs), warps 2..9 softmax (two warps per TMEM lane quarter, 64 of the tile's 128 columns each). The softmax of
-// a tile has two halves, P from S and dS from dP. Where TMEM has room (all but
-// the key side of 128-wide heads) S has two buffers, and P and dS go over the
-// columns of the tile's S, which is dead by then: the next tile's P starts at
-// once, from scores that are already there, and the gradient products and the
-// next dP run under it. Else P goes over S and dS over dP, and the MMAs alternate
-// so that S of the next tile runs while dS is formed.
+// than the tensor pipe does on the MMAs), warps 2..9 softmax (two warps per TMEM
+// lane quarter, 64 of the tile's 128 columns each). The softmax of a tile has two
+// halves, P from S and dS from dP. Where TMEM has room (bf16, all but the key side
+// of 128-wide heads) S has two buffers, and P and dS go over the columns of the
+// tile's S, which is dead by then: the next tile's P starts at once, from scores
+// that are already there, and the gradient products and the next dP run under it.
+// Else P goes over S and dS over dP, and the MMAs alternate so that S of the next
+// tile runs while dS is formed.
 //
 // delta = <o, e> is taken from the bf16 output o, whose rounding matters where
 // few keys average it out; in a sequence's first 128 rows the kernel sums
