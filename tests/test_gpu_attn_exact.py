@@ -356,3 +356,28 @@ def test_offsets_past_32_bits(ctx):
     assert torch.equal(f["O"][2050:], f2["O"]) and torch.equal(f["lse"][2050:], f2["lse"])
     for n in g2:
         assert torch.equal(g[n][2050:], g2[n]), n
+
+
+@pytest.mark.parametrize("dtype,dh", [("bf16", 64), ("bf16", 128), ("f32", 64), ("f32", 32)])
+def test_what_lies_around_a_sequence_does_not_change_its_bits(ctx, dtype, dh):
+    # rows behind (and before) a sequence share its last tile; whether they are a
+    # neighbour's ordinary rows, huge ones, or nobody's, the sequence's results are
+    # those of a call on it alone
+    n, pad, heads, kv = 300, 100, 2, 1
+    base = _inputs(n + 2 * pad, heads, kv, dh, dtype, 31)
+    shape = dict(n_heads=heads, n_kv_heads=kv)
+    alone = [x[pad:pad + n].contiguous() for x in base]
+    f = ctx.attn_forward(*alone[:3], **shape)
+    want = {**f, **ctx.attn_backward(*alone[:3], f["O"], f["lse"], alone[3], **shape)}
+    for size in (1.0, 60.0, 1e4):
+        for cu in ([0, pad, pad + n, n + 2 * pad], [pad, pad + n]):
+            q, k, v, e = (x.clone() for x in base)
+            for x in (q, k, v, e):
+                x[:pad] *= size
+                x[pad + n:] *= size
+            kw = dict(shape, max_len=n, cu_seqlens=torch.tensor(cu, dtype=torch.int32,
+                                                                device="cuda"))
+            f = ctx.attn_forward(q, k, v, **kw)
+            got = {**f, **ctx.attn_backward(q, k, v, f["O"], f["lse"], e, **kw)}
+            for name, x in want.items():
+                assert torch.equal(got[name][pad:pad + n], x), (name, size, cu)

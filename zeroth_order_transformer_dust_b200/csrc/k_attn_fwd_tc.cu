@@ -301,13 +301,15 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
         for (int i = 0; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i >> 5][i & 31]));
       }
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
+      // (a lane past the end has a neighbour's row, or nobody's: it has no vote)
+      const bool grown = __any_sync(0xffffffffu, in && top > m + kGrow);
       if (j == 0) {
         m = top;
       } else if (NP == 3) {
         // (P's third plane has one buffer, so this tile's waits for the product anyway)
         if (!done(j - 1)) break;
         float f = 1.0f;
-        if (__any_sync(0xffffffffu, top > m + kGrow)) {
+        if (grown) {
           const float mn = fmaxf(m, top);
           f = ex2(m - mn);
           m = mn;
@@ -316,7 +318,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
         flush(j - 1, f);
         // (the first half's registers are needed again: the loads below)
         load(0);
-      } else if (__any_sync(0xffffffffu, top > m + kGrow)) {
+      } else if (grown) {
         if (!done(j - 1)) break;  // O holds the tiles before this one
         const float mn = fmaxf(m, top), f = ex2(m - mn);
         m = mn;
