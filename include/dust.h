@@ -364,7 +364,8 @@ typedef struct dust_attn_dims {
   int32_t dtype;             /* of every tensor but lse: DUST_F32 or DUST_BF16 */
   float scale;               /* finite and > 0; 0: 1 / sqrt(head_dim) */
   uint32_t flags;            /* DUST_FLAG_ASYNC */
-  int64_t ldq, ldk, ldv, ldo, lde, lddq, lddk, lddv; /* row strides, elements */
+  int64_t ldq, ldk, ldv, ldo, lde, lddq, lddk, lddv; /* row strides, elements
+                                (not used where T = 1) */
 } dust_attn_dims;
 /* Scratch bytes of dust_attn_forward (backward 0) or dust_attn_backward (1) for
    these dims (cu_seqlens is not read); -1 for invalid dims. Host-only. */

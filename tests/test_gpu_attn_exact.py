@@ -8,6 +8,8 @@ the terms' sizes covers scores up to ~30. bf16 tensors add half a step (2^-8
 relative) wherever the kernels round: the probabilities p and ds that enter a
 product, the output o that delta = <o, e> is formed from, and the result.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -381,3 +383,28 @@ def test_what_lies_around_a_sequence_does_not_change_its_bits(ctx, dtype, dh):
             got = {**f, **ctx.attn_backward(q, k, v, f["O"], f["lse"], e, **kw)}
             for name, x in want.items():
                 assert torch.equal(got[name][pad:pad + n], x), (name, size, cu)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dh", [32, 64, 128])
+@pytest.mark.parametrize("ld", [0, 131, -7])
+def test_one_row_has_no_stride(ctx, dtype, dh, ld):
+    # through the C ABI: the stride of a tensor of one row is not used, whatever it is
+    heads, kv = 2, 1
+    q, k, v, e = _inputs(1, heads, kv, dh, dtype, 6)
+    f = ctx.attn_forward(q, k, v, n_heads=heads, n_kv_heads=kv)
+    want = {**f, **ctx.attn_backward(q, k, v, f["O"], f["lse"], e, n_heads=heads, n_kv_heads=kv)}
+    got = {name: torch.full_like(x, 7.0) for name, x in want.items()}
+    L = dust.load_library()
+    code = dust.DUST_F32 if dtype == "f32" else dust.DUST_BF16
+    d = dust.DustAttnDims(1, None, 1, 1, heads, kv, dh, code, 0.0, 0, *[ld] * 8)
+    work = [torch.empty(max(1, L.dust_attn_work_bytes(ctypes.byref(d), b)), dtype=torch.uint8,
+                        device="cuda") for b in (0, 1)]
+    ctx._bind_stream()
+    ctx._check(L.dust_attn_forward(ctx._h, ctypes.byref(d), *(
+        x.data_ptr() for x in (q, k, v, got["O"], got["lse"], work[0]))))
+    ctx._check(L.dust_attn_backward(ctx._h, ctypes.byref(d), *(
+        x.data_ptr() for x in (q, k, v, got["O"], got["lse"], e, got["dQ"], got["dK"], got["dV"],
+                               work[1]))))
+    for name in want:
+        assert torch.equal(got[name], want[name]), name

@@ -346,6 +346,10 @@ dust_status check_attn_dims(dust_ctx* ctx, const dust_attn_dims* d, AttnArgs* a)
   a->scale = d->scale > 0.0f ? d->scale : 1.0f / std::sqrt((float)d->head_dim);
   a->ldq = d->ldq; a->ldk = d->ldk; a->ldv = d->ldv; a->ldo = d->ldo; a->lde = d->lde;
   a->lddq = d->lddq; a->lddk = d->lddk; a->lddv = d->lddv;
+  if (d->T <= 1) {  // a single row has no stride; the tensor maps still ask for one
+    a->ldq = a->ldo = a->lde = a->lddq = (int64_t)d->n_heads * d->head_dim;
+    a->ldk = a->ldv = a->lddk = a->lddv = (int64_t)d->n_kv_heads * d->head_dim;
+  }
   return DUST_OK;
 }
 
@@ -361,7 +365,7 @@ dust_status check_rows(dust_ctx* ctx, const AttnArgs& a, const char* name, const
   if (a.T > 0 && !p) return fail(ctx, DUST_ERR_ARG, "%s must be non-NULL", name);
   if (!aligned(p, elem_size(a.dtype)))
     return fail(ctx, DUST_ERR_ARG, "%s must be aligned to its elements", name);
-  if (a.T > 1 && (ld < width || ld > (1LL << 31)))
+  if (ld < width || ld > (1LL << 31))
     return fail(ctx, DUST_ERR_ARG, "%s's row stride must lie in [%lld, 2^31]", name,
                 (long long)width);
   return DUST_OK;

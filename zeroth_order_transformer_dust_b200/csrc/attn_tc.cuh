@@ -213,7 +213,7 @@ bool make_map(CUtensorMap* map, const void* p, int64_t T, int64_t cols, int64_t 
 
 // 16-byte rows: what TMA and the vector loads and stores need.
 bool rows16(const AttnArgs& a, const void* p, int64_t ld) {
-  return ((uintptr_t)p & 15) == 0 && (a.T <= 1 || (ld & (a.dtype == DUST_BF16 ? 7 : 3)) == 0);
+  return ((uintptr_t)p & 15) == 0 && (ld & (a.dtype == DUST_BF16 ? 7 : 3)) == 0;
 }
 
 // The tensor maps of n tensors: of the tensors themselves (NP 1), or of their
