@@ -408,3 +408,26 @@ def test_one_row_has_no_stride(ctx, dtype, dh, ld):
                                work[1]))))
     for name in want:
         assert torch.equal(got[name], want[name]), name
+
+
+@pytest.mark.parametrize("dtype,dh", [("bf16", 32), ("bf16", 64), ("bf16", 128), ("f32", 64),
+                                      ("f32", 128)])
+def test_scores_of_minus_infinity_in_the_first_tiles(ctx, dtype, dh):
+    # finite inputs, but the last channel takes the first 140 keys' scores below
+    # fp32's range (-2^129 scale): p = 0 there, and the rows behind attend to the
+    # rest. (The first 140 rows have no other key; they are not looked at.)
+    T, cut = 500, 140
+    q, k, v, e = _inputs(T, 1, 1, dh, dtype, 17)
+    q[:, -1] = 2.0 ** 64
+    k[:, -1] = 0.0
+    k[:cut, -1] = -2.0 ** 65
+    kw = dict(n_heads=1, scale=0.1)
+    f = ctx.attn_forward(q, k, v, **kw)
+    g = ctx.attn_backward(q, k, v, f["O"], f["lse"], e, **kw)
+    ref = oracle.exact_attention(np64(q), np64(k), np64(v), [0, T], 1, 1, kw["scale"], E=np64(e))
+    z, rnd = _sizes(q, k, v, e, torch.from_numpy(ref["O"]), [0, T], 1, 1, kw["scale"])
+    for name, x in (("O", f["O"]), ("dQ", g["dQ"])):
+        tol = F32 * z[name] + HALF[dtype] * (rnd[name] + np.abs(ref[name])) + 1e-30
+        assert np.all((np.abs(np64(x) - ref[name]) <= tol)[cut:]), name
+    err = np.abs(np64(f["lse"]) - ref["lse"])[cut:]
+    assert np.all(err <= F32 * (1 + np.abs(ref["lse"][cut:])))

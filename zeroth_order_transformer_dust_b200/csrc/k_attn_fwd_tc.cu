@@ -29,6 +29,8 @@
 // Warp roles: warp 0 TMA producer, warp 1 issues S products, warp 2 the PV
 // products, warps 4..7 and 8..11 are the softmax of either query tile. Rows past
 // a sequence's end and bounded waits as in k_attn_bwd_tc.cu.
+#include <cfloat>
+
 #include "attn_tc.cuh"
 
 namespace dust {
@@ -304,7 +306,9 @@ __global__ __launch_bounds__(THREADS, 1) void k_attn_fwd_tc(
       // (a lane past the end has a neighbour's row, or nobody's: it has no vote)
       const bool grown = __any_sync(0xffffffffu, in && top > m + kGrow);
       if (j == 0) {
-        m = top;
+        // finite: a tile whose scores are all -inf gives p = 0 and is forgotten by
+        // the first maximum behind it
+        m = fmaxf(top, -FLT_MAX);
       } else if (NP == 3) {
         // (P's third plane has one buffer, so this tile's waits for the product anyway)
         if (!done(j - 1)) break;
