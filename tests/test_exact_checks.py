@@ -163,3 +163,17 @@ def test_null_contexts_and_struct_layout():
     # int64, pointer, int32 x6, float, uint32, int64 x8
     assert ctypes.sizeof(d) == 112 and dust.DustAttnDims.ldq.offset == 48
     assert dust.DustAttnDims.scale.offset == 40
+
+
+def test_scale_that_fp32_does_not_hold():
+    # the struct's scale is fp32, where 0 stands for the default
+    c = _fake_context()
+    x = _t(6, 64)
+    for scale in (1e-50, 1e-46, 0.0, -1e-50, float("nan")):
+        with pytest.raises(ValueError, match="scale"):
+            c.attn_forward(x, x, x, n_heads=1, scale=scale)
+        with pytest.raises(ValueError, match="scale"):
+            c.attn_backward(x, x, x, x, _t(6, 1), x, n_heads=1, scale=scale)
+    assert not [name for name, _ in c._L.calls if name != "dust_attn_work_bytes"]
+    c.attn_forward(x, x, x, n_heads=1, scale=1e-44)
+    assert c._L.calls[-1][1][1]._obj.scale > 0.0

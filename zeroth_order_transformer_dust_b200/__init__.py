@@ -334,8 +334,8 @@ def _exact_attn_dims(Q, K_cache, V_cache, n_heads, n_kv_heads, seq_len, cu_seqle
     dims = DustAttnDims(T, None, 0, 0, n_heads, n_kv_heads, head_dim, _dtype_code(Q),
                         0.0 if scale is None else scale, 0, _row_stride(Q, "Q"),
                         _row_stride(K_cache, "K_cache"), _row_stride(V_cache, "V_cache"))
-    if scale is not None and not scale > 0.0:
-        raise ValueError("scale must be > 0")
+    if scale is not None and not dims.scale > 0.0:  # as fp32 holds it: 0 is the default's mark
+        raise ValueError("scale must be > 0 in fp32")
     if cu_seqlens is not None:
         if seq_len is not None:
             raise ValueError("give seq_len or cu_seqlens, not both")
