@@ -177,3 +177,18 @@ def test_scale_that_fp32_does_not_hold():
     assert not [name for name, _ in c._L.calls if name != "dust_attn_work_bytes"]
     c.attn_forward(x, x, x, n_heads=1, scale=1e-44)
     assert c._L.calls[-1][1][1]._obj.scale > 0.0
+
+
+def test_distill_makes_its_gradient_without_the_room_between_rows():
+    # rows far apart: V wide, each as far from a 16-byte boundary as Z's
+    c = _fake_context()
+    ids, vals = _t(3, 4, dtype=i32), _t(3, 4)
+    for dtype, step in ((f32, 4), (bf16, 8)):
+        for V, ld in ((1001, 50007), (1001, 1001 + 257), (4096, 1 << 20)):
+            Z = torch.zeros(3 * ld, dtype=dtype).view(3, ld)[:, :V]
+            dZ = c.distill(Z, ids, vals)["dZ"]
+            assert tuple(dZ.shape) == (3, V) and dZ.dtype == dtype
+            assert dZ.stride(0) < V + step and (dZ.stride(0) - ld) % step == 0
+            assert c._L.calls[-1][1][13] == dZ.stride(0)
+        Z = torch.zeros(3, 1257, dtype=dtype)[:, :1001]     # a GEMM's padding is kept
+        assert c.distill(Z, ids, vals)["dZ"].stride(0) == 1257

@@ -400,3 +400,18 @@ def test_distill_with_periodic_padding(ctx, every):
     got = ctx.distill(Z, di, dv, weights=dw)
     _check_distill(got, Z, ids, vals, 1.0, w, "bf16")
     assert not got["dZ"][:700].any() and not got["loss"][:700].any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_distill_of_rows_far_apart(ctx, dtype):
+    # the last position of every sequence: rows a whole sequence apart, whose
+    # gradient is made without the room between them
+    B, L, V, k = 5, 40, 3001, 6
+    wide = _logits(B, L * V, dtype, seed=2)
+    Z = wide.view(B, L, V)[:, -1]
+    ids, vals = _teacher(B, V, k, 5)
+    di, dv, _ = _dev(ids, vals)
+    got = ctx.distill(Z, di, dv)
+    _check_distill(got, Z, ids, vals, 1.0, None, dtype)
+    room = got["dZ"].untyped_storage().nbytes()
+    assert room <= B * (V + 8) * (4 if dtype == "f32" else 2)

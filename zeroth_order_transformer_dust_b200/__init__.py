@@ -315,6 +315,14 @@ def _distill_shapes(Z, teacher_ids, teacher_vals, weights):
     return T, V, k, _row_stride(Z, "Z")
 
 
+def _grad_stride(V: int, ld: int, elem_size: int) -> int:
+    """Row stride of a gradient made for V-wide rows of stride ``ld``: theirs,
+    where that is a GEMM's padding, else (rows far apart: a slice of a larger
+    tensor) the least that leaves each row as far from a 16-byte boundary as
+    theirs, which lets the kernel store whole vectors."""
+    return ld if ld - V <= 256 else V + (ld - V) % (16 // elem_size)
+
+
 def _exact_attn_dims(Q, K_cache, V_cache, n_heads, n_kv_heads, seq_len, cu_seqlens, max_len,
                      scale) -> DustAttnDims:
     """Sizes of an attn_forward or attn_backward call (strides of Q, K, V set)."""
@@ -603,9 +611,9 @@ class Context:
         strided) from a teacher's kept entries: teacher_ids (T x k int32, -1:
         none) and teacher_vals (T x k fp32 logits or log probabilities), for
         instance token_logprobs' alternatives of the teacher. "loss" (T,) is
-        temperature^2 KL(teacher || student); "dZ" (T x V, Z's dtype and row
-        stride) the gradient of sum_t weights_t loss_t (weights: T fp32,
-        default 1). Rows of weight 0 or without an entry give zeros.
+        temperature^2 KL(teacher || student); "dZ" (T x V, Z's dtype; Z's row
+        stride where that is V and up to 256 elements of padding) the gradient
+        of sum_t weights_t loss_t (weights: T fp32, default 1). Rows of weight 0 or without an entry give zeros.
         out={"dZ": Z} writes the gradient over the logits."""
         T, V, k, ld = _distill_shapes(Z, teacher_ids, teacher_vals, weights)
         self._cuda(Z, "Z")
@@ -626,10 +634,10 @@ class Context:
                 _check_output(out, "dZ", (T, V), Z.dtype, self.device, rows=True)
                 ldg = _row_stride(out["dZ"], "output dZ")
             else:
-                out["dZ"] = self._empty((T, ld), Z.dtype, Z)
-                if ld != V:
+                ldg = _grad_stride(V, ld, Z.element_size())
+                out["dZ"] = self._empty((T, ldg), Z.dtype, Z)
+                if ldg != V:
                     out["dZ"] = out["dZ"][:, :V]
-                ldg = ld
             dZ = out["dZ"]
         self._bind_stream()
         self._check(self._L.dust_distill(self._h, T, V, _dtype_code(Z), Z.data_ptr(), ld,
