@@ -192,3 +192,26 @@ def test_distill_makes_its_gradient_without_the_room_between_rows():
             assert c._L.calls[-1][1][13] == dZ.stride(0)
         Z = torch.zeros(3, 1257, dtype=dtype)[:, :1001]     # a GEMM's padding is kept
         assert c.distill(Z, ids, vals)["dZ"].stride(0) == 1257
+
+
+def test_streams_without_the_direct_accessor(monkeypatch):
+    # torch's accessor of a stream's handle is not part of its documented
+    # interface: where it is missing, the documented one is used
+    c = _fake_context()
+    del c._bind_stream
+    c.device = 3
+    asked = []
+
+    class Stream:
+        cuda_stream = 77
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: asked.append(d) or Stream())
+    monkeypatch.setattr(dust, "_raw_stream", None)
+    c._bind_stream()
+    assert asked == [3] and _value(c._L.calls[-1][1][1]) == 77
+    monkeypatch.setattr(dust, "_raw_stream", lambda d: 10 + d)
+    c._bind_stream()
+    assert asked == [3] and _value(c._L.calls[-1][1][1]) == 13
+    c._stream = Stream()
+    c._bind_stream()
+    assert _value(c._L.calls[-1][1][1]) == 77

@@ -415,3 +415,22 @@ def test_distill_of_rows_far_apart(ctx, dtype):
     _check_distill(got, Z, ids, vals, 1.0, None, dtype)
     room = got["dZ"].untyped_storage().nbytes()
     assert room <= B * (V + 8) * (4 if dtype == "f32" else 2)
+
+
+def test_the_bound_stream_is_the_current_one(ctx, monkeypatch):
+    # with torch's direct accessor of the stream's handle, and without it
+    bound = []
+
+    class Lib:
+        def dust_set_stream(self, h, s):
+            bound.append(getattr(s, "value", s) or 0)
+
+    monkeypatch.setattr(ctx, "_L", Lib())
+    side = torch.cuda.Stream()
+    for accessor in (dust._raw_stream, None):
+        monkeypatch.setattr(dust, "_raw_stream", accessor)
+        ctx._bind_stream()
+        with torch.cuda.stream(side):
+            ctx._bind_stream()
+    here = torch.cuda.current_stream().cuda_stream
+    assert bound == [here, side.cuda_stream] * 2
