@@ -215,3 +215,31 @@ def test_streams_without_the_direct_accessor(monkeypatch):
     c._stream = Stream()
     c._bind_stream()
     assert _value(c._L.calls[-1][1][1]) == 77
+
+
+def test_packed_rows_beyond_the_longest_sequence():
+    # many packed rows, no max_len: the default stays within what a sequence may have
+    c = _fake_context()
+    T = (1 << 22) + 5
+    x = torch.zeros(1, 64, dtype=bf16).expand(T, 64)
+    cu = torch.tensor([0, 9, T], dtype=i32)
+    dims = dust._exact_attn_dims(_Rows(x), _Rows(x), _Rows(x), 1, None, None, cu, None, None)
+    assert (dims.T, dims.n_seqs, dims.max_len) == (T, 2, 1 << 22)
+    dims = dust._exact_attn_dims(_Rows(x), _Rows(x), _Rows(x), 1, None, None, cu, 77, None)
+    assert dims.max_len == 77
+    small = _t(6, 64)
+    c.attn_forward(small, small, small, n_heads=1, cu_seqlens=torch.tensor([0, 6], dtype=i32))
+    assert c._L.calls[-1][1][1]._obj.max_len == 6
+
+
+class _Rows:
+    """Stands in for a contiguous 2-D tensor of many rows without its memory."""
+
+    def __init__(self, like):
+        self.shape, self.dtype = like.shape, like.dtype
+
+    def dim(self):
+        return 2
+
+    def is_contiguous(self):
+        return True

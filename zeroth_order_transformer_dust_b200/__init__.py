@@ -58,6 +58,7 @@ class DustAttnShape(ctypes.Structure):
 
 
 ATTN_WHICH = {"q": 0, "k": 1, "v": 2}
+MAX_SEQ_LEN = 1 << 22  # rows of a sequence of attn_forward and attn_backward
 
 
 class DustAttnDims(ctypes.Structure):
@@ -355,7 +356,7 @@ def _exact_attn_dims(Q, K_cache, V_cache, n_heads, n_kv_heads, seq_len, cu_seqle
         if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
             raise TypeError("cu_seqlens must be a 1-D int32 tensor of n_seqs + 1 offsets")
         dims.n_seqs = cu_seqlens.numel() - 1
-        dims.max_len = max(T, 1) if max_len is None else max_len
+        dims.max_len = min(max(T, 1), MAX_SEQ_LEN) if max_len is None else max_len
     else:
         length = max(T, 1) if seq_len is None else seq_len
         if length < 1 or T % length:
@@ -661,7 +662,10 @@ class Context:
         (n_kv_heads d_h), fp32 or bf16, d_h 32, 64 or 128; rows may be strided.
         The sequences are of ``seq_len`` rows each, or lie between the offsets
         ``cu_seqlens`` (device int32; ``max_len`` bounds their length, by default
-        T), or are one. ``scale`` defaults to 1 / sqrt(d_h)."""
+        T, at most 2^22; a bound near the longest saves the launch of idle
+        blocks), or are one. ``scale`` defaults to 1 / sqrt(d_h).
+        Rows that no sequence covers are left as they are in the outputs: what
+        an output made by the call holds there is undefined."""
         dims = _exact_attn_dims(Q, K_cache, V_cache, n_heads, n_kv_heads, seq_len, cu_seqlens,
                                 max_len, scale)
         for t, n in ((Q, "Q"), (K_cache, "K_cache"), (V_cache, "V_cache")):
@@ -686,7 +690,8 @@ class Context:
         (like Q) at the attention output: what attn_grad estimates without
         backprop, exactly. O and lse are attn_forward's; the other arguments as
         there. The gradients have the dtype of the inputs; dK and dV sum over
-        the heads that share a key/value head."""
+        the heads that share a key/value head. Rows that no sequence covers are
+        left as they are: give zeroed outputs where all rows enter a sum."""
         dims = _exact_attn_dims(Q, K_cache, V_cache, n_heads, n_kv_heads, seq_len, cu_seqlens,
                                 max_len, scale)
         for t, n in ((O, "O"), (E, "E")):
