@@ -431,3 +431,69 @@ def test_scores_of_minus_infinity_in_the_first_tiles(ctx, dtype, dh):
         assert np.all((np.abs(np64(x) - ref[name]) <= tol)[cut:]), name
     err = np.abs(np64(f["lse"]) - ref["lse"])[cut:]
     assert np.all(err <= F32 * (1 + np.abs(ref["lse"][cut:])))
+
+
+# Sequences of 9 to 14 tiles: every ring of stages is worked through several
+# times, in three heads' turns on the key side, with a ragged last tile. The
+# tolerances hold at these lengths: a chain of n fp32 roundings is off by about
+# sqrt(n) 2^-24 of the sum of the terms' sizes (2.3e-6 for 1500), and an
+# accumulation that truncates once per 16 terms, n / 16 times, by at most
+# n / 16 x 2^-23 of it (1.1e-5), both below F32.
+@pytest.mark.parametrize("dtype,dh", [("bf16", 64), ("bf16", 128), ("f32", 64), ("bf16", 32),
+                                      ("f32", 128)])
+def test_sequences_of_many_tiles(ctx, dtype, dh):
+    _check(ctx, [1409, 0, 1190, 37], 3, 1, dh, dtype, fused=True, first=1, tail=3)
+
+
+@pytest.mark.parametrize("dtype,dh", [("bf16", 128), ("bf16", 64), ("f32", 64)])
+def test_growing_scores_over_many_tiles(ctx, dtype, dh):
+    # the maximum of a row moves in every one of up to ten tiles, or in the first alone
+    T = 1250
+    q, k, v, e = _inputs(T, 1, 1, dh, dtype, 14)
+    ramp = torch.linspace(0.1, 6.0, T, device="cuda")[:, None]
+    for r in (ramp, ramp.flip(0)):
+        kk = (k.float() * r).to(k.dtype)
+        f = ctx.attn_forward(q, kk, v, n_heads=1)
+        g = ctx.attn_backward(q, kk, v, f["O"], f["lse"], e, n_heads=1)
+        ref = oracle.exact_attention(np64(q), np64(kk), np64(v), [0, T], 1, 1, E=np64(e))
+        z, rnd = _sizes(q, kk, v, e, f["O"], [0, T], 1, 1, dh ** -0.5)
+        slack = 100 * 2.0 ** -22   # as in the test of one head width above
+        for name, x in {**f, **g}.items():
+            if name == "lse":
+                assert np.all(np.abs(np64(x) - ref["lse"]) <= 5e-5 * (1 + np.abs(ref["lse"])))
+                continue
+            tol = (F32 + slack) * z[name] + HALF[dtype] * (rnd[name] + np.abs(ref[name])) + 1e-30
+            assert np.all(np.abs(np64(x) - ref[name]) <= tol), name
+
+
+@pytest.mark.parametrize("dtype,dh", [("bf16", 64), ("bf16", 128), ("f32", 64), ("f32", 32)])
+@pytest.mark.parametrize("cu", [[0, 40, 30, 100], [0, 40, 101], [-1, 40, 100], [0, 70, 100],
+                                [0, 40, 200, 100, 100]])
+def test_bad_sequences_stay_as_they_were_and_good_ones_are_computed(ctx, dtype, dh, cu):
+    T, max_len = 100, 64
+    shape = dict(n_heads=2, n_kv_heads=1, max_len=max_len)
+    q, k, v, e = _inputs(T, 2, 1, dh, dtype, 1)
+    offsets = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    new = lambda: {name: torch.full((T, w), 7.0, dtype=dt, device="cuda")  # noqa: E731
+                   for name, w, dt in (("O", 2 * dh, q.dtype), ("lse", 2, torch.float32),
+                                       ("dQ", 2 * dh, q.dtype), ("dK", dh, q.dtype),
+                                       ("dV", dh, q.dtype))}
+    part = lambda out, names: {n: out[n] for n in names}  # noqa: E731
+    want, got = new(), new()
+    good = [(a, b) for a, b in zip(cu[:-1], cu[1:]) if 0 <= a <= b <= T and b - a <= max_len]
+    for a, b in good:
+        kw = dict(shape, cu_seqlens=torch.tensor([a, b], dtype=torch.int32, device="cuda"))
+        ctx.attn_forward(q, k, v, out=part(want, ("O", "lse")), **kw)
+        ctx.attn_backward(q, k, v, want["O"], want["lse"], e, out=part(want, ("dQ", "dK", "dV")),
+                          **kw)
+    for call in (lambda: ctx.attn_forward(q, k, v, out=part(got, ("O", "lse")),
+                                          cu_seqlens=offsets, **shape),
+                 lambda: ctx.attn_backward(q, k, v, want["O"], want["lse"], e,
+                                           out=part(got, ("dQ", "dK", "dV")),
+                                           cu_seqlens=offsets, **shape)):
+        with pytest.raises(dust.DustError) as err:
+            call()
+        assert err.value.status == 4
+    ctx.check()                               # reported once
+    for name in want:
+        assert torch.equal(got[name], want[name]), name

@@ -434,3 +434,52 @@ def test_the_bound_stream_is_the_current_one(ctx, monkeypatch):
             ctx._bind_stream()
     here = torch.cuda.current_stream().cuda_stream
     assert bound == [here, side.cuda_stream] * 2
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_distill_clusters_work_through_several_rows(ctx, dtype):
+    # rows of two (bf16) and three (fp32) CTAs, about three to five live rows for
+    # every cluster that is resident at once: the exchange of the CTAs' sums and
+    # the copies of the next row take turns. Every fifth row is padding, and some
+    # clusters get a run of it; rows of odd pitch, then the same in place.
+    T, V, k = 450, 60001, 9
+    Z = _logits(T, V, dtype, seed=7, pitch=V + 2, offset=1)
+    ids, vals = _teacher(T, V, k, 8)
+    w = np.linspace(0.5, 1.5, T).astype(np.float32)
+    w[4::5] = 0.0
+    w[60:110] = 0.0
+    di, dv, dw = _dev(ids, vals, w)
+    for _ in range(2):
+        got = ctx.distill(Z, di, dv, weights=dw, temperature=1.3)
+    _check_distill(got, Z, ids, vals, 1.3, w, dtype)
+    assert not got["dZ"][60:110].any() and not got["loss"][60:110].any()
+    again = ctx.distill(Z, di, dv, weights=dw, temperature=1.3, out={"dZ": Z})
+    assert torch.equal(again["dZ"], got["dZ"]) and torch.equal(again["loss"], got["loss"])
+
+
+@pytest.mark.parametrize("how", ["weight", "entry"])
+@pytest.mark.parametrize("T,V", [(4000, 2003), (900, 60001)])
+def test_distill_writes_zeros_for_every_row_left_out(ctx, T, V, how):
+    # many more rows than CTAs, six of them live: the others hold NaN, before the
+    # call and in the gradient's memory, and come out as zeros
+    k = 5
+    Z = torch.full((T, V), math.nan, dtype=torch.bfloat16, device="cuda")
+    live = np.array([0, 3, T // 2, T // 2 + 1, T - 100, T - 1])
+    Z[torch.from_numpy(live).cuda()] = _logits(6, V, "bf16", seed=4)
+    ids, vals = _teacher(T, V, k, 4, missing=False)
+    w = np.ones(T, dtype=np.float32)
+    out = np.setdiff1d(np.arange(T), live)
+    if how == "weight":
+        w[out] = 0.0
+    else:
+        ids[out] = -1
+    di, dv, dw = _dev(ids, vals, w)
+    for dZ in (torch.full_like(Z, math.nan), Z):
+        rows = Z[torch.from_numpy(live).cuda()].clone()
+        got = ctx.distill(Z, di, dv, weights=dw, out={
+            "dZ": dZ, "loss": torch.full((T,), math.nan, device="cuda")})
+        gone = torch.from_numpy(out).cuda()
+        assert not got["dZ"][gone].any() and not got["loss"][gone].any()
+        kept = torch.from_numpy(live).cuda()
+        _check_distill({"dZ": got["dZ"][kept], "loss": got["loss"][kept]}, rows, ids[live],
+                       vals[live], 1.0, None, "bf16")
