@@ -483,3 +483,26 @@ def test_distill_writes_zeros_for_every_row_left_out(ctx, T, V, how):
         kept = torch.from_numpy(live).cuda()
         _check_distill({"dZ": got["dZ"][kept], "loss": got["loss"][kept]}, rows, ids[live],
                        vals[live], 1.0, None, "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("tau", [0.25, 0.5, 1.0, 3.0])
+@pytest.mark.parametrize("V", [300, 60001])
+def test_distill_where_the_student_has_the_lowest_value(ctx, dtype, tau, V):
+    # a kept token whose logit is the type's lowest value, a mask that is finite:
+    # the loss is tau q 3.4e38, which fp32 holds (q is about 1e-6 for one such
+    # entry, and 1 for all of them where tau < 1)
+    T, k = 4, 5
+    Z = _logits(T, V, dtype, seed=9)
+    ids, vals = _teacher(T, V, k, 10, missing=False)
+    vals[:, 1] = vals.max(1) - 14.0 * tau
+    for t in range(T - 1):
+        Z[t, ids[t, 1]] = torch.finfo(DT[dtype]).min
+    if tau < 1.0:                             # the whole of the teacher's weight
+        Z[0, ids[0]] = torch.finfo(DT[dtype]).min
+    di, dv, _ = _dev(ids, vals)
+    got = ctx.distill(Z, di, dv, temperature=tau)
+    assert torch.isfinite(got["loss"]).all()
+    _check_distill(got, Z, ids, vals, tau, None, dtype)
+    only = ctx.distill(Z, di, dv, temperature=tau, want_grad=False)
+    torch.testing.assert_close(only["loss"], got["loss"], rtol=2e-5, atol=2e-5 * tau ** 2)

@@ -825,9 +825,11 @@ __global__ __launch_bounds__(MODE == kLossOnly ? kLpThreads
       const float q = eq / qsum;
       float part = 0.0f;
       if (my_id >= 0 && q != 0.0f) {
-        // (log s = -inf for a row of -inf: log p = -inf, loss = +inf)
-        const float lp = all.s == 0.0f ? -inf_f() : (zj - all.m) / a.tau - logf(all.s);
-        part = q * (dv - logf(qsum) - lp);
+        // tau^2 q (log q - log p) with the temperature kept off the differences: the
+        // lowest finite logit stays finite (s = 0: a row of -inf, loss +inf)
+        const float d = (my_v - vm) - (zj - all.m);
+        part = all.s == 0.0f ? inf_f()
+                             : a.tau * q * (d + a.tau * (logf(all.s) - logf(qsum)));
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
@@ -899,7 +901,7 @@ __global__ __launch_bounds__(MODE == kLossOnly ? kLpThreads
     sync_threads(THREADS);  // the row's shared values and dense stores are done
     if (mine) store_e(out + my_id, fix);
     if (rank == 0 && tid == 0 && a.loss)
-      a.loss[t] = a.tau * a.tau * ((sh.loss[0] + sh.loss[1]) + (sh.loss[2] + sh.loss[3]));
+      a.loss[t] = (sh.loss[0] + sh.loss[1]) + (sh.loss[2] + sh.loss[3]);
     t = tn;
   }
   if (ranks > 1) ptx::cluster_sync();  // the others' shared memory is no longer read
