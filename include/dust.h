@@ -94,7 +94,7 @@ typedef struct dust_params {
    (a cudaStream_t; NULL = the legacy default stream). Environment variables
    read here select alternative kernels of the context (all give the same
    results within the parity tolerances): DUST_DISABLE_TC=1 runs every GEMM
-   on CUDA cores; DUST_TC_PAIR=0 gives each tensor-core GEMM tile one CTA
+   and the exact attention on CUDA cores; DUST_TC_PAIR=0 gives each tensor-core GEMM tile one CTA
    instead of a CTA pair; DUST_SUBSET_KERNEL=1 uses the L2-fed subset-draw
    kernel instead of the shared-memory one; DUST_FULL_KERNEL=2 runs
    full-vocabulary draws as a reward pass and a g pass (the noise generated
@@ -304,8 +304,11 @@ dust_status dust_attn_grad(dust_ctx* ctx, const dust_params* p, const dust_attn_
  * logits, the rest of its alternatives are id -1 with log probability -inf; a
  * row of -inf alone has logp -inf and entropy 0. A row that holds NaN or +inf
  * has no distribution: logp, entropy and top_logp are NaN, its ids -1.
+ * T in [0, 2^27], V in [1, 2^31), strides up to 2^40 (not used where T = 1).
  * Needs no scratch. T = 0 launches nothing. flags: DUST_FLAG_ASYNC. The call
- * does not clear the status that earlier DUST_FLAG_ASYNC calls left.
+ * does not clear the status that earlier DUST_FLAG_ASYNC calls left, so without
+ * the flag it reports theirs, too (the estimators' calls do clear it: check
+ * before them).
  * Errors: DUST_ERR_ARG, DUST_ERR_BOUNDS (a token outside [-1, V): its logp is NaN).
  */
 dust_status dust_token_logprobs(dust_ctx* ctx, int64_t T, int64_t V, int32_t dtype, const void* Z,
@@ -335,6 +338,7 @@ dust_status dust_token_logprobs(dust_ctx* ctx, int64_t T, int64_t V, int32_t dty
  * 0, and its logits are not read. A masked student logit (-inf) has p = 0; the
  * loss is +inf where the teacher keeps it. NaN and +inf logits of a row make
  * its loss and gradient NaN. The gradient is formed in fp32 and rounded once.
+ * temperature in [1e-6, 1e6]; T, V and strides as for dust_token_logprobs.
  * Needs no scratch. T = 0 launches nothing. flags as dust_token_logprobs.
  * Errors: DUST_ERR_ARG, DUST_ERR_BOUNDS (a teacher id outside [-1, V), which
  * counts as no entry), DUST_ERR_TIMEOUT.
@@ -354,18 +358,20 @@ dust_status dust_distill(dust_ctx* ctx, int64_t T, int64_t V, int32_t dtype, con
  * n_heads / n_kv_heads consecutive ones share a key/value head.
  */
 typedef struct dust_attn_dims {
-  int64_t T;                 /* rows of the tensors */
+  int64_t T;                 /* rows of the tensors, below 2^31 */
   const int32_t* cu_seqlens; /* DEVICE, n_seqs + 1 non-decreasing row offsets in
                                 [0, T]; NULL: n_seqs sequences of max_len rows */
-  int32_t n_seqs;            /* sequences (0: nothing is launched), at most 65535 */
-  int32_t max_len;           /* longest sequence (>= 1) */
+  int32_t n_seqs;            /* sequences (0: nothing is launched), at most 65535;
+                                n_seqs n_heads below 2^31 */
+  int32_t max_len;           /* longest sequence, in [1, 2^22]; blocks are launched
+                                for n_seqs sequences of this length */
   int32_t n_heads, n_kv_heads; /* n_heads a multiple of n_kv_heads, at most 65535 */
   int32_t head_dim;          /* 32, 64 or 128 */
   int32_t dtype;             /* of every tensor but lse: DUST_F32 or DUST_BF16 */
   float scale;               /* finite and > 0; 0: 1 / sqrt(head_dim) */
   uint32_t flags;            /* DUST_FLAG_ASYNC */
-  int64_t ldq, ldk, ldv, ldo, lde, lddq, lddk, lddv; /* row strides, elements
-                                (not used where T = 1) */
+  int64_t ldq, ldk, ldv, ldo, lde, lddq, lddk, lddv; /* row strides, elements,
+                                up to 2^31 (not used where T = 1) */
 } dust_attn_dims;
 /* Scratch bytes of dust_attn_forward (backward 0) or dust_attn_backward (1) for
    these dims (cu_seqlens is not read); -1 for invalid dims. Host-only. */
@@ -373,13 +379,20 @@ int64_t dust_attn_work_bytes(const dust_attn_dims* dims, int backward);
 /* Forward.
  *   Q T x (n_heads head_dim), Kc and Vc T x (n_kv_heads head_dim)
  *   O_out   like Q; lse_out T x n_heads fp32, log-sum-exp of a row's scores
- * Rows that no sequence covers (behind the last one, say) are neither read nor
- * written, and neither is anything of one sequence mixed into another, NaN
- * included. Values that are not finite spread inside their own sequence.
+ * Rows that no sequence covers (behind the last one, say) are not written, and
+ * what they hold enters no result (they may be loaded with the rows beside them);
+ * nor does anything of one sequence enter another's, NaN included: a sequence's
+ * outputs have the same bits whatever lies around it. Values that are not finite
+ * spread inside their own sequence. A row whose scores are all -inf has no
+ * distribution: O NaN, lse not finite.
  * fp32 tensors keep fp32 accuracy (64-wide heads run on the tensor cores in
  * three bf16 planes per operand, other widths on CUDA cores). bf16 tensors:
- * products with fp32 accumulation, softmax in fp32, the probabilities rounded
- * to bf16 for the product with V; outputs are rounded once.
+ * products with fp32 accumulation, softmax in fp32. On the tensor cores (64- and
+ * 128-wide heads, every tensor's rows on 16-byte boundaries) the probabilities are
+ * rounded to bf16 for the product with V, half a step (2^-8 relative) per term:
+ * against 64 bits O is 2.0e-3 off (relative norm) where its own rounding alone
+ * makes 1.6e-3. On CUDA cores (32-wide heads, rows off those boundaries) they stay
+ * in fp32. Outputs are rounded once.
  *   work     the caller's scratch, dust_attn_work_bytes(dims, 0) bytes, 256-byte
  *            aligned, overwritten; NULL: fp32 tensors run on CUDA cores
  * The call has no scratch of its own, so calls and captured graphs that overlap
@@ -396,8 +409,12 @@ dust_status dust_attn_forward(dust_ctx* ctx, const dust_attn_dims* dims, const v
  *   dQ_out   like Q; dK_out, dV_out like Kc (sums over the heads that share
  *            a key/value head); dtype as the inputs, rounded once
  *   work     as above, dust_attn_work_bytes(dims, 1) bytes, not NULL
- * The probabilities are recomputed from lse; no sum uses atomics, so results
- * are the same from run to run. Outputs must not overlap the inputs or one
+ * The probabilities P are recomputed from lse; no sum uses atomics, so results
+ * are the same from run to run. bf16 tensors on the tensor cores (as above):
+ * P and dS = P (dP - delta) are rounded to bf16 for their products, and delta =
+ * <o, e> takes O as it is, rounded, except in a sequence's first 128 rows: 2.4e-3
+ * off against 64 bits where the gradients' own rounding alone makes 1.7e-3. On
+ * CUDA cores P and dS stay in fp32. Outputs must not overlap the inputs or one
  * another (the same address is refused; interleaved columns of one tensor are
  * not an overlap).
  * Errors as dust_attn_forward. */

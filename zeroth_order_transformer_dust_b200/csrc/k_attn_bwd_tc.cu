@@ -50,11 +50,14 @@
 // Measured (query side + key side): 8 x 1024 tokens, 12 heads of 64, bf16 60 + 70 us
 // (0.25 PFLOP/s of the exact flops); packed sequences of 3000 to 1000, 16 query and
 // 4 key/value heads of 128, bf16 167 + 228 us (0.50 PFLOP/s); the first in fp32
-// planes 38 + 170 + 137 + 161 us. A tile takes about 2100 cycles with 64-wide heads
-// and 2500 to 4000 with 128-wide ones, against 770 to 2050 of MMAs: the chain of
-// hand-overs S -> P -> sum -> S bounds it, then a CTA's start of 4000 cycles, of
-// which 64-wide heads have one every four tiles. The key side of grouped heads
-// also waits for its longest CTA (94 tiles where the mean SM has 70).
+// planes 38 + 170 + 137 + 161 us. By stamps inside one CTA a tile takes about 2100
+// cycles with 64-wide heads and 2500 to 4000 with 128-wide ones, against 770 to
+// 2050 of MMAs: the chain of hand-overs S -> P -> sum -> S; a CTA's start takes
+// 4000. That does not account for the whole: the first case's query side has 23.4
+// tiles and 5.2 starts an SM, 36 of its 60 us, and the rest (the sums' way out,
+// one CTA's end and the next one's launch, the last wave) has not been stamped.
+// The key side of grouped heads also waits for its longest CTA (94 tiles where
+// the mean SM has 70).
 //
 // Every wait is bounded: on expiry the CTA raises the timeout bit, drains its own
 // copies and MMAs (bounded again), frees its TMEM and returns.

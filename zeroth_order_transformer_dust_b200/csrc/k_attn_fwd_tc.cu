@@ -23,8 +23,9 @@
 // total in fp32, rounded (1.9e-6 off over a sequence of 1024 without that).
 //
 // Measured: packed sequences of 3000 to 1000, 16 query and 4 key/value heads of
-// 128, bf16 121 us (0.65 PFLOP/s of the exact flops); 8 x 1024 tokens, 12 heads of
-// 64, fp32 29 us for the planes and 134 us.
+// 128, bf16 117 us (0.67 PFLOP/s of the exact flops); 8 x 1024 tokens, 12 heads of
+// 64, bf16 46 us (0.28), fp32 160 us with the 29 for its planes; 12 heads of 128,
+// bf16 57 us (0.46).
 //
 // Warp roles: warp 0 TMA producer, warp 1 issues S products, warp 2 the PV
 // products, warps 4..7 and 8..11 are the softmax of either query tile. Rows past

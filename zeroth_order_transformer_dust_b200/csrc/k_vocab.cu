@@ -237,12 +237,13 @@ __device__ __forceinline__ Stat stat_cluster(const Stat& a, float k2, Stat* mine
 // first tiles (n elements at least are not below it), so on ordinary rows about
 // n (1 + ln(V / tile)) elements ever enter. Cutting at 2 n entries and not at 512
 // took 4096 x 128256 fp32 with n = 64 from 790 to 467 us together with the
-// cheaper ordering; without alternatives the same logits take 316 us (6.7 TB/s,
-// the copy rate). 8192 x 50257 bf16: 150 us, 5.5 TB/s. 4 x 128256 fp32 with n =
-// 20, eight CTAs a row: 13 us, 7 of them for the statistics alone. Any row is
-// handled: a tile that
-// enters whole fits the list. List order depends on timing, the sorted list
-// does not: keys are (value, ~index), all different.
+// cheaper ordering (443 and 470 us on two cards since); without alternatives the
+// same logits take 303 us, 6.9 TB/s: reads alone run above the rate of a copy,
+// 6.55. 8192 x 50257 bf16: 157 and 167 us on two cards, 5.2 and 4.9 TB/s; with n =
+// 20, 360 us. 4 x 128256 fp32 with n = 20, eight CTAs a row: 13 us, 7 of them for
+// the statistics alone. Any row is handled: a tile that enters whole fits the
+// list. List order depends on timing, the sorted list does not: keys are (value,
+// ~index), all different.
 constexpr int kLpThreads = 256;
 constexpr int kTopTile = 8;                           // elements per thread and tile
 constexpr int kTopTileElems = kLpThreads * kTopTile;  // a tile
@@ -551,13 +552,15 @@ __global__ __launch_bounds__(kLpThreads, TOP || sizeof(E) == 2 ? 4 : 3) void k_t
 // buffers (kReread) are read from global memory twice. The loss alone is a
 // streaming pass.
 //
-// Measured: 8192 x 50304 bf16 (a tenth of the rows left out) 358 us, 4.4 TB/s;
-// 2048 x 128256 fp32 417 us, 4.8 TB/s; the loss of 1000 x 50304 fp32 37 us, 5.4
-// TB/s. The gradient takes two exponentials per logit, and without them the same
-// copies and stores take 266 and 375 us: what is left is the exponentials' issue
-// slots, not the memory. The copies are a warp's own: refilled by one of the
-// computing threads, which then waits for the others chunk by chunk, the first
-// case took 583 us.
+// Measured: 8192 x 50304 bf16 (a tenth of the rows left out) 367 us, 4.3 TB/s;
+// 2048 x 128256 fp32 418 us, 4.8 TB/s; the loss of 1000 x 50304 fp32 39 us, 5.1
+// TB/s (bf16 27 us, 3.7). The gradient takes two exponentials per logit, and
+// without them the same copies and stores take 266 and 375 us: what is left is the
+// exponentials' issue slots, not the memory. The copies are a warp's own: refilled
+// by one of the computing threads, which then waits for the others chunk by chunk,
+// the first case took 583 us. A row per CTA or cluster and nothing kept for the
+// next, the form this one replaced, took 357 us there and 517 in the second case:
+// one form serves both types, at 3 % of the first and a fifth off the second.
 enum DistillMode { kLossOnly = 0, kResident = 1, kReread = 2 };
 constexpr int kDsThreads = 480;             // (loss alone: kLpThreads, for more rows at a time)
 constexpr int kMaxTeacher = kTopLimit;
