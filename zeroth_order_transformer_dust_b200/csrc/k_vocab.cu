@@ -552,15 +552,16 @@ __global__ __launch_bounds__(kLpThreads, TOP || sizeof(E) == 2 ? 4 : 3) void k_t
 // buffers (kReread) are read from global memory twice. The loss alone is a
 // streaming pass.
 //
-// Measured: 8192 x 50304 bf16 (a tenth of the rows left out) 367 us, 4.3 TB/s;
-// 2048 x 128256 fp32 418 us, 4.8 TB/s; the loss of 1000 x 50304 fp32 39 us, 5.1
+// Measured: 8192 x 50304 bf16 (a tenth of the rows left out) 351 us, 4.5 TB/s;
+// 2048 x 128256 fp32 415 us, 4.8 TB/s; the loss of 1000 x 50304 fp32 39 us, 5.1
 // TB/s (bf16 27 us, 3.7). The gradient takes two exponentials per logit, and
 // without them the same copies and stores take 266 and 375 us: what is left is the
 // exponentials' issue slots, not the memory. The copies are a warp's own: refilled
 // by one of the computing threads, which then waits for the others chunk by chunk,
 // the first case took 583 us. A row per CTA or cluster and nothing kept for the
-// next, the form this one replaced, took 357 us there and 517 in the second case:
-// one form serves both types, at 3 % of the first and a fifth off the second.
+// next, the form this one replaced, took 357 us there and 517 in the second case.
+// The loss costs the gradient time, too: a division by tau less at each kept entry
+// (log p is not formed, only its difference times tau) took 366 us to 351.
 enum DistillMode { kLossOnly = 0, kResident = 1, kReread = 2 };
 constexpr int kDsThreads = 480;             // (loss alone: kLpThreads, for more rows at a time)
 constexpr int kMaxTeacher = kTopLimit;
